@@ -75,7 +75,7 @@ def draw(rng):
                 return c
     fmt = rng.choice(("mxfp4", "nvfp4", "int4", "int4"))
     group = rng.choice((32, 64, 128)) if fmt == "int4" else 0
-    unit = group or {"mxfp4": 32, "nvfp4": 16}[fmt]
+    unit = group or 32
     while True:
         geglu = rng.random() < 0.25
         N, K = _log(rng, 1, 131072), unit * _log(rng, 1, 16384 // unit)
