@@ -63,6 +63,7 @@
  *     launches nothing.  MOE_ERR_HIP reports a launch failure; faults during
  *     execution surface at the caller's next synchronisation.  No C++
  *     exception crosses this interface.
+ *   - moe_forward_few and moe_gemv_w4 state their own limits below.
  *   - Supported sizes: H % 64 == 0, I % 64 == 0, 1 <= k <= min(E, 32),
  *     E <= 1024, T*k < 2^30.  Pointers to bf16 arrays, x_perm, h and y must
  *     be 16-byte aligned (W4A4 weight codes too), the other arrays 4-byte
@@ -115,6 +116,12 @@ typedef struct moe_shape {
  * six significant bits), with fp32 sums scaled by the weight's matrix scale
  * times g.  Through moe_forward only; not with a dense MLP. */
 enum { MOE_W_BF16 = 0, MOE_W_MXFP4 = 1, MOE_W_MXFP4_A4 = 2, MOE_W_NVFP4 = 3, MOE_W_NVFP4_A4 = 4 };
+
+/* moe_gemv_w4 only: INT4 codes (two per byte, the even K index in the low
+ * nibble) with one bf16 scale, and optionally one zero point, per group of
+ * 32, 64 or 128 consecutive K values of a row; a weight is scale x (code -
+ * zero), code 0..15. */
+enum { MOE_W_INT4 = 5 };
 
 /* Bytes in front of the E4M3 codes of an NVFP4 scale buffer: the E fp32
  * matrix scales and one fp32 activation input scale (slot E, read by
@@ -320,6 +327,95 @@ int moe_forward_noalloc(const moe_shape *s, const uint16_t *x, const uint16_t *w
  */
 int moe_quantize_nv(const uint16_t *src, int64_t rows, int32_t K, const float *input_scale,
                     uint8_t *codes, uint8_t *scales, moe_stream_t stream);
+
+/* Largest token count of moe_forward_few and moe_gemv_w4. */
+#define MOE_FEW_MAX_TOKENS 16
+/* Leading workspace bytes of moe_forward_few and moe_gemv_w4 that must start
+ * out zero. */
+#define MOE_FEW_ZERO_BYTES 4096
+
+/*
+ * moe_forward_few -- the whole layer for T <= MOE_FEW_MAX_TOKENS tokens in
+ * one kernel launch: router, selection, gate/up + GEGLU, down and the
+ * weighted sum, with the dense GEGLU MLP of moe_forward_shared added when
+ * I_sh > 0.  Routing (ids, weights) is bit for bit that of moe_route; h is
+ * rounded to bf16 as in moe_forward, the experts' outputs are not rounded
+ * before they are weighted and summed (fp32), and out is rounded once.
+ * Results do not depend on how the work was scheduled: the same call gives
+ * the same bits.
+ *   weights, scales  as for moe_forward / moe_forward_shared; formats
+ *                    MOE_W_BF16, MOE_W_MXFP4 and MOE_W_NVFP4 (the dense MLP
+ *                    in the experts' format too, an NVFP4 one with a scale
+ *                    buffer for E = 1); 4-bit codes 16-byte aligned
+ *   I_sh             0 (no dense MLP: its four arguments are ignored) or a
+ *                    positive multiple of 64
+ *   out              [T][H] bf16 out, no overlap with the inputs
+ *   topk_ids_out     [T][k] int32 out or NULL;  topk_w_out [T][k] fp32 or NULL
+ *   ws               device scratch of at least moe_few_workspace_bytes(s,
+ *                    I_sh), 16-byte aligned.  Its first MOE_FEW_ZERO_BYTES
+ *                    must be zero before the first call with it, and every
+ *                    call leaves them zero; a workspace may be shared by
+ *                    calls (of moe_gemv_w4 too) that do not overlap in time.
+ *                    With other contents the results are undefined (the
+ *                    kernel still ends).
+ * MOE_ERR_UNSUPPORTED for T above the limit and the W4A4 formats.  Non-finite
+ * values in a token's x affect that token's output only.
+ */
+int moe_forward_few(const moe_shape *s, const uint16_t *x, const uint16_t *w_router,
+                    const float *router_bias, const void *w_gate_up, const uint8_t *gu_scales,
+                    const void *w_down, const uint8_t *d_scales, int32_t I_sh,
+                    const void *w_sh_gate_up, const uint8_t *sh_gu_scales, const void *w_sh_down,
+                    const uint8_t *sh_d_scales, uint16_t *out, int32_t *topk_ids_out,
+                    float *topk_w_out, void *ws, size_t ws_bytes, moe_stream_t stream);
+
+/* Workspace bytes moe_forward_few needs; 0 for a shape it does not take or an
+ * I_sh that is neither 0 nor a positive multiple of 64. */
+size_t moe_few_workspace_bytes(const moe_shape *s, int32_t I_sh);
+
+typedef struct moe_w4_shape {
+    int32_t T;        /* rows of x, 1 .. MOE_FEW_MAX_TOKENS */
+    int32_t N;        /* weight rows, 1 .. 2^30 */
+    int32_t K;        /* weight columns: a multiple of 32 and of the group, at most 2^20 */
+    int32_t w_format; /* MOE_W_MXFP4, MOE_W_NVFP4 or MOE_W_INT4 */
+    int32_t group;    /* MOE_W_INT4: 32, 64 or 128; otherwise 0 */
+    int32_t flags;    /* MOE_GEMV_GEGLU, MOE_GEMV_Y_FP32 or both, or 0 */
+    int64_t ldx, ldy; /* elements between rows of x (a multiple of 8, >= K) and of y; 0: dense */
+} moe_w4_shape;
+
+enum {
+    MOE_GEMV_GEGLU = 1,  /* y = gelu_tanh(gate) * up: gate the first N/2 rows of W (N even) */
+    MOE_GEMV_Y_FP32 = 2  /* y in fp32 instead of bf16 */
+};
+
+/*
+ * moe_gemv_w4 -- product of up to MOE_FEW_MAX_TOKENS tokens with a 4-bit
+ * weight matrix: y[t][n] = sum_k x[t][k] W[n][k] (+ bias[n]), fp32 sums, or
+ * with MOE_GEMV_GEGLU y[t][c] = gelu_tanh(a[t][c]) * a[t][N/2 + c] of those
+ * a; rounded once.  The dense matrices of a decode step in the experts'
+ * formats (the block's MLP, projections, output logits).
+ *   x       [T][ldx] bf16, 16-byte aligned
+ *   w       [N][K/2] codes, 16-byte aligned
+ *   scales  MXFP4: E8M0 [N][K/32]; NVFP4: a scale buffer for E = 1 (header,
+ *           then E4M3 [N][K/16]), 4-byte aligned; INT4: bf16 [N][K/group],
+ *           2-byte aligned
+ *   zeros   MOE_W_INT4: uint8 [N][K/group] or NULL (8 everywhere); otherwise
+ *           NULL
+ *   bias    [N] fp32 or NULL
+ *   y       [T][ldy] out (N, or N/2 columns with GEGLU), bf16 (2-byte
+ *           aligned) or fp32 (4-byte aligned); what lies between the rows is
+ *           not written
+ *   ws      device scratch of at least moe_gemv_w4_workspace_bytes(s), with
+ *           the zero-prefix rule of moe_forward_few; may be NULL when that is 0
+ * A non-finite value in a row of x makes that row's outputs non-finite
+ * (INT4: NaN) and affects no other row.  The same call gives the same bits.
+ */
+int moe_gemv_w4(const moe_w4_shape *s, const uint16_t *x, const uint8_t *w, const uint8_t *scales,
+                const uint8_t *zeros, const float *bias, void *y, void *ws, size_t ws_bytes,
+                moe_stream_t stream);
+
+/* Workspace bytes moe_gemv_w4 needs for this shape (0: none needed, or an
+ * invalid shape). */
+size_t moe_gemv_w4_workspace_bytes(const moe_w4_shape *s);
 
 /* Workspace bytes moe_forward needs for this shape; 0 for an invalid or
  * unsupported shape.  Monotone in T. */

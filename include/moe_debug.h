@@ -27,7 +27,8 @@ extern "C" {
  *   violations  out: accesses redirected since the last read
  *   where       out: 0 if none, else 100000 * f + line: the source file f
  *               (1 routing, 2 permutation, 3 grouped GEMM, 4 combine,
- *               5 quantisers) and line of the first violation in it
+ *               5 quantisers, 6 few-token layer, 7 4-bit matrix-vector product)
+ *               and line of the first violation in it
  * Returns MOE_OK, MOE_ERR_INVALID_ARGUMENT (NULL pointer) or MOE_ERR_HIP.
  */
 int moe_debug_bounds(uint32_t *violations, uint32_t *where);

@@ -10,6 +10,12 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmoe.so")
 
 MOE_W_BF16, MOE_W_MXFP4, MOE_W_MXFP4_A4, MOE_W_NVFP4, MOE_W_NVFP4_A4 = 0, 1, 2, 3, 4
+MOE_W_INT4 = 5          # moe_gemv_w4 only
+MOE_GEMV_GEGLU, MOE_GEMV_Y_FP32 = 1, 2
+# MOE_FEW_MAX_TOKENS: the most tokens moe_forward_few and moe_gemv_w4 take.
+FEW_MAX_TOKENS = 16
+# MOE_FEW_ZERO_BYTES: leading bytes of their workspace that start out zero.
+FEW_ZERO_BYTES = 4096
 MOE_FORWARD_STAGES = 5
 STATUS = {0: "MOE_OK", -1: "MOE_ERR_INVALID_ARGUMENT", -2: "MOE_ERR_UNSUPPORTED",
           -3: "MOE_ERR_WORKSPACE", -4: "MOE_ERR_HIP", -5: "MOE_ERR_SCRATCH_TOO_SMALL"}
@@ -20,7 +26,8 @@ NOALLOC_SCRATCH_BYTES = 64 << 20
 EXPORTS = ("moe_route", "moe_permute", "moe_grouped_gemm_gateup", "moe_grouped_gemm_down",
            "moe_combine", "moe_forward", "moe_forward_shared", "moe_workspace_bytes",
            "moe_workspace_shared_bytes", "moe_route_workspace_bytes", "moe_permute_workspace_bytes",
-           "moe_quantize_mx", "moe_quantize_nv", "moe_forward_noalloc", "moe_status_string")
+           "moe_quantize_mx", "moe_quantize_nv", "moe_forward_noalloc", "moe_status_string",
+           "moe_forward_few", "moe_few_workspace_bytes", "moe_gemv_w4", "moe_gemv_w4_workspace_bytes")
 
 
 class MoeShape(ctypes.Structure):
@@ -32,6 +39,16 @@ class MoeShape(ctypes.Structure):
                 f"w_format={self.w_format})")
 
 
+class MoeW4Shape(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("w_format", ctypes.c_int32),
+                ("group", ctypes.c_int32), ("flags", ctypes.c_int32), ("ldx", ctypes.c_int64),
+                ("ldy", ctypes.c_int64)]
+
+    def __repr__(self):
+        return (f"MoeW4Shape(T={self.T}, N={self.N}, K={self.K}, w_format={self.w_format}, group={self.group}, "
+                f"flags={self.flags}, ldx={self.ldx}, ldy={self.ldy})")
+
+
 class MoeError(RuntimeError):
     def __init__(self, fn, status, msg):
         super().__init__(f"{fn} failed: {STATUS.get(status, status)} ({msg})")
@@ -41,6 +58,7 @@ class MoeError(RuntimeError):
 _lib = None
 _P = ctypes.c_void_p
 _S = ctypes.POINTER(MoeShape)
+_S4 = ctypes.POINTER(MoeW4Shape)
 
 
 def load(path: str = LIB_PATH):
@@ -64,6 +82,9 @@ def load(path: str = LIB_PATH):
         "moe_forward_noalloc": [_S, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P],
         "moe_forward_shared": [_S, _P, _P, _P, _P, _P, _P, _P, ctypes.c_int32, _P, _P, _P, _P, _P, _P, _P, _P,
                                c_size, _P, _P],
+        "moe_forward_few": [_S, _P, _P, _P, _P, _P, _P, _P, ctypes.c_int32, _P, _P, _P, _P, _P, _P, _P, _P, c_size,
+                            _P],
+        "moe_gemv_w4": [_S4, _P, _P, _P, _P, _P, _P, _P, c_size, _P],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -79,6 +100,10 @@ def load(path: str = LIB_PATH):
     lib.moe_quantize_nv.restype = c_int
     lib.moe_workspace_shared_bytes.argtypes = [_S, ctypes.c_int32]
     lib.moe_workspace_shared_bytes.restype = c_size
+    lib.moe_few_workspace_bytes.argtypes = [_S, ctypes.c_int32]
+    lib.moe_few_workspace_bytes.restype = c_size
+    lib.moe_gemv_w4_workspace_bytes.argtypes = [_S4]
+    lib.moe_gemv_w4_workspace_bytes.restype = c_size
     lib.moe_status_string.argtypes = [c_int]
     lib.moe_status_string.restype = ctypes.c_char_p
     _lib = lib
@@ -91,6 +116,18 @@ def shape(T, H, E, k, I, mxfp4=False, a4=False, nvfp4=False, nv_a4=False) -> Moe
     else:
         fmt = MOE_W_MXFP4_A4 if a4 else (MOE_W_MXFP4 if mxfp4 else MOE_W_BF16)
     return MoeShape(T, H, E, k, I, fmt)
+
+
+W4_FORMATS = {"mxfp4": MOE_W_MXFP4, "nvfp4": MOE_W_NVFP4, "int4": MOE_W_INT4}
+
+
+def w4_shape(T, N, K, fmt, group=0, geglu=False, y_fp32=False, ldx=0, ldy=0) -> MoeW4Shape:
+    """Shape of moe_gemv_w4; fmt is "mxfp4", "nvfp4" or "int4" (with its
+    group), ldx and ldy the row strides of x and y in elements (0: dense)."""
+    if fmt not in W4_FORMATS:
+        raise ValueError(f"unknown 4-bit format {fmt!r}: one of {sorted(W4_FORMATS)}")
+    flags = (MOE_GEMV_GEGLU if geglu else 0) | (MOE_GEMV_Y_FP32 if y_fp32 else 0)
+    return MoeW4Shape(T, N, K, W4_FORMATS[fmt], group, flags, ldx, ldy)
 
 
 def nvfp4_header_bytes(E: int) -> int:
@@ -242,3 +279,48 @@ def quantize_mx(src, codes, scales, stream=None):
     lib = load()
     rows, K = src.shape
     _check("moe_quantize_mx", lib.moe_quantize_mx(_ptr(src), rows, K, _ptr(codes), _ptr(scales), _stream(stream)))
+
+
+def few_workspace_bytes(s: MoeShape, I_sh: int = 0) -> int:
+    return load().moe_few_workspace_bytes(ctypes.byref(s), I_sh)
+
+
+def gemv_w4_workspace_bytes(s: MoeW4Shape) -> int:
+    return load().moe_gemv_w4_workspace_bytes(ctypes.byref(s))
+
+
+def forward_few(s, x, w_router, router_bias, w_gate_up, gu_scales, w_down, d_scales, out, topk_ids_out=None,
+                topk_w_out=None, ws=None, I_sh=0, w_sh_gate_up=None, sh_gu_scales=None, w_sh_down=None,
+                sh_d_scales=None, stream=None):
+    """moe_forward_few: the whole layer for up to FEW_MAX_TOKENS tokens in one
+    launch (ws: device.few_workspace), with a dense GEGLU MLP of intermediate
+    I_sh added when I_sh > 0."""
+    lib = load()
+    nbytes = ws.numel() * ws.element_size() if ws is not None else 0
+    _check("moe_forward_few",
+           lib.moe_forward_few(ctypes.byref(s), _ptr(x), _ptr(w_router), _ptr(router_bias), _ptr(w_gate_up),
+                               _ptr(gu_scales), _ptr(w_down), _ptr(d_scales), I_sh, _ptr(w_sh_gate_up),
+                               _ptr(sh_gu_scales), _ptr(w_sh_down), _ptr(sh_d_scales), _ptr(out),
+                               _ptr(topk_ids_out), _ptr(topk_w_out), _ptr(ws), nbytes, _stream(stream)))
+
+
+def _rows_ptr(t, ld, name):
+    """Device address of a [T][cols] tensor whose rows are `ld` elements apart
+    (0: dense) and contiguous themselves."""
+    if not ld or isinstance(t, int):
+        return _ptr(t)
+    if not t.is_cuda:
+        raise ValueError("expected a device tensor")
+    if t.dim() != 2 or t.stride(1) != 1 or (t.shape[0] > 1 and t.stride(0) != ld):
+        raise ValueError(f"{name} is not rows of stride {ld}")
+    return t.data_ptr()
+
+
+def gemv_w4(s: MoeW4Shape, x, w, scales, zeros, bias, y, ws=None, stream=None):
+    """moe_gemv_w4: y = x W^T for up to FEW_MAX_TOKENS rows of x and 4-bit W
+    (ws: device.gemv_workspace where gemv_w4_workspace_bytes is not 0)."""
+    lib = load()
+    nbytes = ws.numel() * ws.element_size() if ws is not None else 0
+    _check("moe_gemv_w4",
+           lib.moe_gemv_w4(ctypes.byref(s), _rows_ptr(x, s.ldx, "x"), _ptr(w), _ptr(scales), _ptr(zeros), _ptr(bias),
+                           _rows_ptr(y, s.ldy, "y"), _ptr(ws), nbytes, _stream(stream)))

@@ -152,6 +152,82 @@ Workspace carve(const moe_shape *s, void *base, int I_sh = 0) {
     return w;
 }
 
+// moe_forward_few's workspace.
+struct FewWorkspace {
+    uint32_t *counters;
+    float *logits;
+    uint16_t *h, *h_sh;
+    size_t bytes;
+};
+
+FewWorkspace carve_few(const moe_shape *s, void *base, int I_sh) {
+    char *p = static_cast<char *>(base);
+    size_t off = 0;
+    FewWorkspace w{};
+    auto take = [&](size_t bytes) {
+        char *q = p ? p + off : nullptr;
+        off += round_up(bytes);
+        return q;
+    };
+    w.counters = reinterpret_cast<uint32_t *>(take(MOE_FEW_ZERO_BYTES));
+    w.logits = reinterpret_cast<float *>(take((size_t)s->T * s->E * sizeof(float)));
+    w.h = reinterpret_cast<uint16_t *>(take((size_t)s->T * s->k * s->I * sizeof(uint16_t)));
+    w.h_sh = I_sh > 0 ? reinterpret_cast<uint16_t *>(take((size_t)s->T * I_sh * sizeof(uint16_t))) : nullptr;
+    w.bytes = off;
+    return w;
+}
+static_assert(moe::kFewCounterBytes <= MOE_FEW_ZERO_BYTES, "counters of the few-token layer");
+static_assert(moe::kFewMaxT == MOE_FEW_MAX_TOKENS, "tokens of the few-token kernels");
+
+int check_few(const moe_shape *s, int32_t I_sh) {
+    const int st = check_shape(s);
+    if (st != MOE_OK) return st;
+    if (I_sh < 0) return MOE_ERR_INVALID_ARGUMENT;
+    if (s->T > MOE_FEW_MAX_TOKENS || I_sh % 64 != 0) return MOE_ERR_UNSUPPORTED;
+    if (s->w_format == MOE_W_MXFP4_A4 || s->w_format == MOE_W_NVFP4_A4) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+// An expert (or dense MLP, E = 1) weight argument of moe_forward_few.
+int check_few_weights(const moe_shape *s, const void *w, const uint8_t *scales) {
+    const int st = check_weights(s, w, scales);
+    if (st != MOE_OK) return st;
+    return al16(w) ? MOE_OK : MOE_ERR_INVALID_ARGUMENT;
+}
+
+moe::FewWeights few_weights(const moe_shape *s, int E, const void *w, const uint8_t *scales) {
+    if (!is_nvfp4(s)) return {w, scales, nullptr};
+    return {w, scales + MOE_NVFP4_HEADER_BYTES(E), reinterpret_cast<const float *>(scales)};
+}
+
+// Largest N and K of moe_gemv_w4 (the index arithmetic's range; a K this long
+// is 256 K ranges of 16 tokens, one counter each at most).
+constexpr int kGemvMaxN = 1 << 30, kGemvMaxK = 1 << 20;
+
+int check_w4(const moe_w4_shape *s) {
+    if (!s) return MOE_ERR_INVALID_ARGUMENT;
+    if (s->T < 1 || s->N < 1 || s->K < 1 || s->group < 0 || s->ldx < 0 || s->ldy < 0) return MOE_ERR_INVALID_ARGUMENT;
+    if (s->flags & ~(MOE_GEMV_GEGLU | MOE_GEMV_Y_FP32)) return MOE_ERR_INVALID_ARGUMENT;
+    const bool i4 = s->w_format == MOE_W_INT4;
+    if (!i4 && s->w_format != MOE_W_MXFP4 && s->w_format != MOE_W_NVFP4) return MOE_ERR_UNSUPPORTED;
+    if (!i4 && s->group != 0) return MOE_ERR_INVALID_ARGUMENT;
+    if (i4 && s->group != 32 && s->group != 64 && s->group != 128) return MOE_ERR_UNSUPPORTED;
+    if (s->T > MOE_FEW_MAX_TOKENS || s->N > kGemvMaxN || s->K > kGemvMaxK) return MOE_ERR_UNSUPPORTED;
+    if (s->K % 32 != 0 || (i4 && s->K % s->group != 0)) return MOE_ERR_UNSUPPORTED;
+    if ((s->flags & MOE_GEMV_GEGLU) && s->N % 2 != 0) return MOE_ERR_INVALID_ARGUMENT;
+    const int outs = s->flags & MOE_GEMV_GEGLU ? s->N / 2 : s->N;
+    if (s->ldx && (s->ldx < s->K || s->ldx >= (int64_t{1} << 40))) return MOE_ERR_INVALID_ARGUMENT;
+    if (s->ldx % 8 != 0) return MOE_ERR_UNSUPPORTED;
+    if (s->ldy && (s->ldy < outs || s->ldy >= (int64_t{1} << 40))) return MOE_ERR_INVALID_ARGUMENT;
+    return MOE_OK;
+}
+
+size_t gemv_ws(const moe_w4_shape *s) {
+    const size_t part =
+        moe::gemv_part_bytes(moe::gemv_plan(s->T, s->N, s->K, s->flags & MOE_GEMV_GEGLU), s->T);
+    return part ? MOE_FEW_ZERO_BYTES + round_up(part) : 0;
+}
+
 int hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 
 // Device address of `scratch` on each device, looked up once per device
@@ -476,15 +552,105 @@ int moe_quantize_nv(const uint16_t *src, int64_t rows, int32_t K, const float *i
                                               static_cast<hipStream_t>(stream)));
 }
 
+size_t moe_few_workspace_bytes(const moe_shape *s, int32_t I_sh) {
+    if (check_few(s, I_sh) != MOE_OK) return 0;
+    return carve_few(s, nullptr, I_sh).bytes;
+}
+
+int moe_forward_few(const moe_shape *s, const uint16_t *x, const uint16_t *w_router, const float *router_bias,
+                    const void *w_gate_up, const uint8_t *gu_scales, const void *w_down, const uint8_t *d_scales,
+                    int32_t I_sh, const void *w_sh_gate_up, const uint8_t *sh_gu_scales, const void *w_sh_down,
+                    const uint8_t *sh_d_scales, uint16_t *out, int32_t *topk_ids_out, float *topk_w_out, void *ws,
+                    size_t ws_bytes, moe_stream_t stream) {
+    int st = check_few(s, I_sh);
+    if (st != MOE_OK) return st;
+    if (!x || !w_router || !out || !al16(x) || !al16(w_router) || !al16(out)) return MOE_ERR_INVALID_ARGUMENT;
+    if ((router_bias && !al4(router_bias)) || (topk_ids_out && !al4(topk_ids_out)) || (topk_w_out && !al4(topk_w_out)))
+        return MOE_ERR_INVALID_ARGUMENT;
+    if ((st = check_few_weights(s, w_gate_up, gu_scales)) != MOE_OK) return st;
+    if ((st = check_few_weights(s, w_down, d_scales)) != MOE_OK) return st;
+    if (I_sh > 0) {
+        if ((st = check_few_weights(s, w_sh_gate_up, sh_gu_scales)) != MOE_OK) return st;
+        if ((st = check_few_weights(s, w_sh_down, sh_d_scales)) != MOE_OK) return st;
+    }
+    if (!ws || ws_bytes < carve_few(s, nullptr, I_sh).bytes || !al16(ws)) return MOE_ERR_WORKSPACE;
+    const FewWorkspace w = carve_few(s, ws, I_sh);
+    moe::FewLayer l{};
+    l.x = x;
+    l.w_router = w_router;
+    l.bias = router_bias;
+    l.gate_up = few_weights(s, s->E, w_gate_up, gu_scales);
+    l.down = few_weights(s, s->E, w_down, d_scales);
+    if (I_sh > 0) {
+        l.sh_gate_up = few_weights(s, 1, w_sh_gate_up, sh_gu_scales);
+        l.sh_down = few_weights(s, 1, w_sh_down, sh_d_scales);
+    }
+    l.fmt = weight_view(s, gu_scales).fmt;
+    l.out = out;
+    l.ids = topk_ids_out;
+    l.w = topk_w_out;
+    l.counters = w.counters;
+    l.logits = w.logits;
+    l.h = w.h;
+    l.h_sh = w.h_sh;
+    l.T = s->T;
+    l.H = s->H;
+    l.E = s->E;
+    l.k = s->k;
+    l.I = s->I;
+    l.I_sh = I_sh;
+    return hip_status(moe::launch_few_layer(l, static_cast<hipStream_t>(stream)));
+}
+
+size_t moe_gemv_w4_workspace_bytes(const moe_w4_shape *s) {
+    if (check_w4(s) != MOE_OK) return 0;
+    return gemv_ws(s);
+}
+
+int moe_gemv_w4(const moe_w4_shape *s, const uint16_t *x, const uint8_t *w, const uint8_t *scales,
+                const uint8_t *zeros, const float *bias, void *y, void *ws, size_t ws_bytes, moe_stream_t stream) {
+    const int st = check_w4(s);
+    if (st != MOE_OK) return st;
+    const bool i4 = s->w_format == MOE_W_INT4, nv = s->w_format == MOE_W_NVFP4;
+    const bool y_fp32 = s->flags & MOE_GEMV_Y_FP32, geglu = s->flags & MOE_GEMV_GEGLU;
+    if (!x || !w || !scales || !y || !al16(x) || !al16(w)) return MOE_ERR_INVALID_ARGUMENT;
+    if ((nv && !al4(scales)) || (i4 && (reinterpret_cast<uintptr_t>(scales) & 1u))) return MOE_ERR_INVALID_ARGUMENT;
+    if ((zeros && !i4) || (bias && !al4(bias))) return MOE_ERR_INVALID_ARGUMENT;
+    if (reinterpret_cast<uintptr_t>(y) & (y_fp32 ? 3u : 1u)) return MOE_ERR_INVALID_ARGUMENT;
+    const size_t need = gemv_ws(s);
+    if (need && (!ws || ws_bytes < need || !al16(ws))) return MOE_ERR_WORKSPACE;
+    moe::GemvW4 l{};
+    l.x = x;
+    l.w = w;
+    l.scales = nv ? scales + MOE_NVFP4_HEADER_BYTES(1) : scales;
+    l.zeros = zeros;
+    l.global = nv ? reinterpret_cast<const float *>(scales) : nullptr;
+    l.bias = bias;
+    l.y = y;
+    l.counters = need ? static_cast<uint32_t *>(ws) : nullptr;
+    l.part = need ? reinterpret_cast<float *>(static_cast<char *>(ws) + MOE_FEW_ZERO_BYTES) : nullptr;
+    l.ldx = s->ldx ? s->ldx : s->K;
+    l.ldy = s->ldy ? s->ldy : (geglu ? s->N / 2 : s->N);
+    l.T = s->T;
+    l.N = s->N;
+    l.K = s->K;
+    l.group = s->group;
+    l.fmt = i4 ? moe::GemvFormat::kINT4 : (nv ? moe::GemvFormat::kNVFP4 : moe::GemvFormat::kMXFP4);
+    l.geglu = geglu;
+    l.y_fp32 = y_fp32;
+    return hip_status(moe::launch_gemv_w4(l, static_cast<hipStream_t>(stream)));
+}
+
 #ifdef MOE_DEBUG
 int moe_debug_bounds(uint32_t *violations, uint32_t *where) {
     if (!violations || !where) return MOE_ERR_INVALID_ARGUMENT;
     hipError_t (*const readers[])(uint32_t *) = {moe::debug_read_route, moe::debug_read_permute,
                                                  moe::debug_read_gemm, moe::debug_read_combine,
-                                                 moe::debug_read_quant};
+                                                 moe::debug_read_quant, moe::debug_read_few,
+                                                 moe::debug_read_gemv};
     *violations = 0;
     *where = 0;
-    for (int i = 0; i < 5; ++i) {
+    for (int i = 0; i < 7; ++i) {
         uint32_t rec[2] = {0u, 0u};
         if (readers[i](rec) != hipSuccess) return MOE_ERR_HIP;
         if (rec[0] && !*violations) *where = 100000u * (uint32_t)(i + 1) + rec[1];

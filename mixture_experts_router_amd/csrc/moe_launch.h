@@ -103,6 +103,52 @@ hipError_t launch_quantize_nv(const uint16_t *src, long long rows, int K, const 
 hipError_t launch_combine(const uint16_t *y, const int32_t *inv, const float *w, const float *y_sh32, int nsplit,
                           uint16_t *out, int T, int H, int k, hipStream_t st);
 
+// The whole layer for up to kFewMaxT tokens in one launch.  A weight argument:
+// bf16 values or 4-bit codes, block scales, (NVFP4) the fp32 matrix scales.
+constexpr int kFewMaxT = 16;
+struct FewWeights {
+    const void *w;
+    const uint8_t *scales;
+    const float *global;
+};
+struct FewLayer {
+    const uint16_t *x, *w_router;
+    const float *bias;
+    FewWeights gate_up, down, sh_gate_up, sh_down;   // the dense MLP's only with I_sh > 0
+    WeightFormat fmt;
+    uint16_t *out;
+    int32_t *ids;            // or nullptr
+    float *w;                // or nullptr
+    uint32_t *counters;      // kFewCounterBytes, zero before the launch and after it
+    float *logits;           // [T][E]
+    uint16_t *h, *h_sh;      // [T*k][I], [T][I_sh]
+    int T, H, E, k, I, I_sh;
+};
+constexpr int kFewCounterBytes = 512;
+hipError_t launch_few_layer(const FewLayer &l, hipStream_t st);
+
+// Matrix-vector products with 4-bit weights for up to kFewMaxT tokens.
+enum class GemvFormat { kMXFP4, kNVFP4, kINT4 };
+struct GemvPlan {
+    int outs, units, ranges, slices;
+};
+GemvPlan gemv_plan(int T, int N, int K, bool geglu);
+size_t gemv_part_bytes(const GemvPlan &g, int T);   // 0: no workspace needed
+struct GemvW4 {
+    const uint16_t *x;
+    const uint8_t *w, *scales, *zeros;   // zeros (INT4) or nullptr: 8
+    const float *global;                 // NVFP4 matrix scale
+    const float *bias;                   // or nullptr
+    void *y;
+    float *part;                         // gemv_part_bytes
+    uint32_t *counters;                  // one per range, zero before the launch and after it
+    long long ldx, ldy;
+    int T, N, K, group;
+    GemvFormat fmt;
+    bool geglu, y_fp32;
+};
+hipError_t launch_gemv_w4(const GemvW4 &l, hipStream_t st);
+
 #ifdef MOE_DEBUG
 // Bounds-check records of the MOE_DEBUG build, one per source file: rec[0]
 // violations, rec[1] source line of the first; each read clears the record.
@@ -111,6 +157,8 @@ hipError_t debug_read_permute(uint32_t *rec);
 hipError_t debug_read_gemm(uint32_t *rec);
 hipError_t debug_read_combine(uint32_t *rec);
 hipError_t debug_read_quant(uint32_t *rec);
+hipError_t debug_read_few(uint32_t *rec);
+hipError_t debug_read_gemv(uint32_t *rec);
 #endif
 
 }  // namespace moe

@@ -18,6 +18,7 @@
 #include "moe_common.h"
 #include "moe_launch.h"
 #include "permute_block.h"
+#include "topk.h"
 
 namespace moe {
 
@@ -83,30 +84,6 @@ __global__ __launch_bounds__(256) void router_partial_kernel(const uint16_t *__r
 }
 
 // ---------------------------------------------------------------- top-k
-// Order-preserving integer key of a float: larger float -> larger key.
-// -0.0 is mapped to +0.0 so equal values tie.
-__device__ __forceinline__ uint32_t order_key(float v) {
-    const uint32_t u = __float_as_uint(v == 0.f ? 0.f : v);
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-__device__ __forceinline__ float key_value(uint32_t k) {
-    return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
-}
-
-// Wave-wide maximum in every lane: DPP steps inside each row of 16 lanes
-// (quad swaps, then the half-row and row mirrors), then the gfx950 lane swaps
-// between the two halves and between neighbouring rows.
-__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
-    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));    // quad [1,0,3,2]
-    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));    // quad [2,3,0,1]
-    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, false));   // row_half_mirror
-    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, false));   // row_mirror
-    const auto h = __builtin_amdgcn_permlane32_swap(v, v, false, false);   // lanes l and l ^ 32
-    v = max(h[0], h[1]);
-    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);   // rows 0<->1, 2<->3
-    return max(r[0], r[1]);
-}
-
 // Top-k of one token by one wave; lane l holds experts e = l + 64 i.  Slot j
 // takes the largest remaining key, the lowest expert index among equal keys
 // (so slots come out ordered by logit descending, index ascending), and the
@@ -170,40 +147,11 @@ __device__ __forceinline__ void topk_token(int t, const float *__restrict__ part
             key[i] = e < E ? order_key(*MOE_CHECKED(logits + (size_t)t * E + e, 4, logits, (size_t)T * E * 4)) : 0u;
         }
     }
-    // k rounds of wave argmax; lane j keeps slot j.
-    int my_idx = 0;
-    uint32_t my_key = 0;
-    for (int j = 0; j < k; ++j) {
-        uint32_t lm = key[0];
-#pragma unroll
-        for (int i = 1; i < VPL; ++i) lm = max(lm, key[i]);
-        const uint32_t km = wave_max_u32(lm);
-        // the lowest expert index holding km: the lowest lane of the lowest
-        // i with a hit (scalar selects, no branch per i)
-        int sel = 0;
-#pragma unroll
-        for (int i = VPL - 1; i >= 0; --i) {
-            const uint64_t hit = __ballot(key[i] == km);
-            // (bit 63 keeps the count defined for an empty mask, whose
-            // result is not selected, and changes no nonzero one)
-            sel = hit ? 64 * i + (int)__builtin_ctzll(hit | (1ull << 63)) : sel;
-        }
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            if (64 * i + lane == sel) key[i] = 0u;
-        if (lane == j) {
-            my_idx = sel;
-            my_key = km;
-        }
-    }
-    // weights: exp(l_j - l_0) in every slot lane at once, their sum in slot order
-    const float top = key_value((uint32_t)__builtin_amdgcn_readfirstlane((int)my_key));
-    const float ex = lane < k ? expf(key_value(my_key) - top) : 0.f;
-    float sum = 0.f;
-    for (int m = 0; m < k; ++m) sum += __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, ex), m));
+    int my_idx;
+    const float my_w = topk_slots<VPL>(key, k, my_idx);
     if (lane < k) {
         *MOE_CHECKED(ids + (size_t)t * k + lane, 4, ids, (size_t)T * k * 4) = my_idx;
-        *MOE_CHECKED(wts + (size_t)t * k + lane, 4, wts, (size_t)T * k * 4) = ex / sum;
+        *MOE_CHECKED(wts + (size_t)t * k + lane, 4, wts, (size_t)T * k * 4) = my_w;
         if (lds_ids) lds_ids[t * k + lane] = my_idx;
     }
 }

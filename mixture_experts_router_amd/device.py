@@ -35,6 +35,20 @@ def workspace(s, device="cuda", I_sh: int = 0):
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
+def few_workspace(s, device="cuda", I_sh: int = 0):
+    """moe_forward_few workspace, zero-filled: its leading MOE_FEW_ZERO_BYTES
+    must start at zero (each call leaves them zero)."""
+    import torch
+    return torch.zeros(_lib.few_workspace_bytes(s, I_sh), dtype=torch.uint8, device=device)
+
+
+def gemv_workspace(s, device="cuda"):
+    """moe_gemv_w4 workspace, zero-filled, or None where the shape needs none."""
+    import torch
+    n = _lib.gemv_w4_workspace_bytes(s)
+    return torch.zeros(n, dtype=torch.uint8, device=device) if n else None
+
+
 _hip = None
 
 
