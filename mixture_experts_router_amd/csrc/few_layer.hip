@@ -15,12 +15,13 @@
 //            routing weights multiply the fp32 sums, experts are added in a
 //            fixed order, and out is rounded once
 //
-// Work items are handed out by a ticket counter, router items first, then
-// gate/up, then down.  A workgroup waits only for items of an earlier phase,
-// and all of those have been taken by workgroups that are running when a
-// later ticket is handed out: every wait ends, whatever else runs on the GPU
-// and however few workgroups are resident.
+// Each phase's items are handed out by a ticket counter.  A workgroup takes
+// router items while there are any, then gate/up shares, then down items, and
+// waits only for items of an earlier phase, all of which have then been taken
+// by workgroups that are running: every wait ends, whatever else runs on the
+// GPU and however few workgroups are resident.
 #include <algorithm>
+#include <type_traits>
 
 #include "few_stream.h"
 #include "moe_launch.h"
@@ -30,12 +31,13 @@ namespace moe {
 
 namespace {
 
-constexpr int kFewWaves = 8;
+constexpr int kFewWaves = 8, kFewThreads = 64 * kFewWaves;
 constexpr int kFewXBytes = 128 * 1024;                    // token rows in LDS
 constexpr int kFewMaxA = kFewTokens * 32;                 // assignments (k <= 32)
 
 // Counters in the workspace's zeroed prefix, a line each.
-constexpr int kCtrTicket = 0, kCtrRouter = 32, kCtrGateUp = 64, kCtrExit = 96;
+constexpr int kCtrRouterTicket = 0, kCtrGateUpTicket = 32, kCtrDownTicket = 64;   // next item of each phase
+constexpr int kCtrRouter = 96, kCtrGateUp = 128, kCtrExit = 160;                    // items done, workgroups left
 
 struct FewArgs {
     const uint16_t *x, *wr;
@@ -51,7 +53,7 @@ struct FewArgs {
     float *logits;
     uint16_t *h, *h_sh;                         // [T k][I], [T][I_sh]
     int T, H, E, k, I, I_sh;
-    int n_router, n_gu_sh, n_gu, n_down;        // tickets of each kind
+    int n_router, n_gu, n_down;                 // items of each phase
 };
 
 struct FewSmem {
@@ -63,7 +65,7 @@ struct FewSmem {
     int16_t expert[kFewMaxA];                   // touched experts, ascending
     int16_t index[1024];                        // expert -> touched index (or -1)
     int n_experts;
-    int ticket;
+    int ticket, down;
 };
 static_assert(sizeof(FewSmem) <= 160 * 1024, "LDS of one workgroup");
 
@@ -71,29 +73,43 @@ __device__ __forceinline__ uint32_t ctr_add(uint32_t *p) {
     return __hip_atomic_fetch_add(p, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// Publishes what this workgroup has written: every wave's stores are
-// complete, then one thread makes them visible device-wide and counts.
-__device__ __forceinline__ void publish(uint32_t *ctr) {
+// Publishes what this workgroup has written (every wave's stores are complete,
+// then one thread makes them visible device-wide and counts) and takes the
+// next ticket of the phase.  Both happen in one branch of thread 0, and
+// barriers stand on either side of it: two such branches with no barrier
+// between them, as at the end and the start of a loop's body, may be joined by
+// the compiler across the back edge, which lets the other lanes run ahead.
+__device__ __forceinline__ int publish_and_next(uint32_t *done, uint32_t *tickets, int *slot) {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     if (threadIdx.x == 0) {
         __threadfence();
-        ctr_add(ctr);
-    }
-}
-
-// Waits until `n` workgroups have published.  The count is reached as long as
-// the counters were zero before the launch; the bound only keeps a workspace
-// that was not from holding the GPU (its results are then undefined).
-__device__ __forceinline__ void wait_for(uint32_t *ctr, uint32_t n) {
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < (1 << 22); ++i) {
-            if (__hip_atomic_load(ctr, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) >= n) break;
-            __builtin_amdgcn_s_sleep(1);
-        }
-        __threadfence();
+        ctr_add(done);
+        *slot = (int)ctr_add(tickets);
     }
     __syncthreads();
+    return uniform(*slot);
+}
+
+// One thread waits until `n` workgroups have published, and makes what they
+// wrote visible to its workgroup, which joins a barrier next: the caches'
+// invalidation is complete, not merely requested, before the others load.
+// The count is reached as long as the counters were zero before the launch;
+// the bound only keeps a workspace that was not from holding the GPU (its
+// results are then undefined).
+__device__ __forceinline__ void wait_count(uint32_t *ctr, uint32_t n) {
+    for (int i = 0; i < (1 << 20); ++i) {
+        if (__hip_atomic_load(ctr, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) >= n) break;
+        __builtin_amdgcn_s_sleep(1);
+    }
+    __threadfence();
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
+// Share i of n of `units` units: as even as whole units allow.
+__device__ __forceinline__ int share_start(int i, int units, int n) {
+    const int q = units / n, r = units - q * n;
+    return i * q + min(i, r);
 }
 
 // ---------------------------------------------------------------- router
@@ -101,7 +117,7 @@ __device__ __forceinline__ void wait_for(uint32_t *ctr, uint32_t n) {
 // values, each summed in fp32 by MFMAs in K order; one thread per (token,
 // expert) adds the chunk sums in fp64 in chunk order.
 __device__ void few_router(const FewArgs &p, FewSmem &sm, int item) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
+    const int lane = threadIdx.x & 63, wave = wave_index(), r = lane & 15, g = lane >> 4;
     const int e0 = 4 * item, nchunks = (p.H + 255) / 256;
     const bool on_e = r < 4 && e0 + r < p.E, on_t = r < p.T;
     f32x4(*sum)[kFewTokens] = reinterpret_cast<f32x4(*)[kFewTokens]>(sm.red);   // [16 chunks][token]
@@ -136,7 +152,6 @@ __device__ void few_router(const FewArgs &p, FewSmem &sm, int item) {
         const double b = p.bias ? (double)p.bias[e0 + et] : 0.0;
         *MOE_CHECKED(p.logits + (size_t)tt * p.E + e0 + et, 4, p.logits, (size_t)p.T * p.E * 4) = (float)(total + b);
     }
-    publish(p.ctr + kCtrRouter);
 }
 
 template <int VPL>
@@ -163,10 +178,11 @@ __device__ __forceinline__ void few_topk(const FewArgs &p, FewSmem &sm, int t, b
 // The routing of every token, by each workgroup for itself: ids and weights,
 // the touched experts in ascending order and who goes there.
 __device__ void few_select(const FewArgs &p, FewSmem &sm, bool store) {
-    wait_for(p.ctr + kCtrRouter, p.n_router);
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, A = p.T * p.k;
-    for (int i = threadIdx.x; i < 1024; i += blockDim.x) sm.index[i] = -1;
-    for (int i = threadIdx.x; i < kFewMaxA * kFewTokens / 4; i += blockDim.x) reinterpret_cast<uint32_t *>(sm.slot)[i] = 0u;
+    const int wave = wave_index(), lane = threadIdx.x & 63, A = p.T * p.k;
+    for (int i = threadIdx.x; i < p.E; i += kFewThreads) sm.index[i] = -1;
+    for (int i = threadIdx.x; i < A * kFewTokens / 4; i += kFewThreads) reinterpret_cast<uint32_t *>(sm.slot)[i] = 0u;
+    if (threadIdx.x == 0) wait_count(p.ctr + kCtrRouter, p.n_router);
+    __syncthreads();
     for (int t = wave; t < p.T; t += kFewWaves) {
         if (p.E <= 64) few_topk<1>(p, sm, t, store);
         else if (p.E <= 128) few_topk<2>(p, sm, t, store);
@@ -175,7 +191,7 @@ __device__ void few_select(const FewArgs &p, FewSmem &sm, bool store) {
         else few_topk<16>(p, sm, t, store);
     }
     __syncthreads();
-    for (int a = threadIdx.x; a < A; a += blockDim.x) sm.index[sm.ids[a]] = 0;
+    for (int a = threadIdx.x; a < A; a += kFewThreads) sm.index[sm.ids[a]] = 0;
     __syncthreads();
     if (wave == 0) {
         int n = 0;
@@ -192,7 +208,7 @@ __device__ void few_select(const FewArgs &p, FewSmem &sm, bool store) {
         if (lane == 0) sm.n_experts = n;
     }
     __syncthreads();
-    for (int a = threadIdx.x; a < A; a += blockDim.x)
+    for (int a = threadIdx.x; a < A; a += kFewThreads)
         sm.slot[sm.index[sm.ids[a]]][a / p.k] = (uint8_t)(a % p.k + 1);
     __syncthreads();
 }
@@ -200,10 +216,10 @@ __device__ void few_select(const FewArgs &p, FewSmem &sm, bool store) {
 // ---------------------------------------------------------------- gate/up
 // The token operand of MFMA f, lane (r, g): from LDS, where every fragment
 // has 16 bytes per (g, token), or from the rows of x.
-template <int F>
-__device__ __forceinline__ u32x4 few_x_frag(const FewArgs &p, const FewSmem &sm, bool in_lds, int f, int r, int g) {
+template <int F, bool XL>
+__device__ __forceinline__ u32x4 few_x_frag(const FewArgs &p, const FewSmem &sm, int f, int r, int g) {
     const int t = min(r, p.T - 1);
-    if (in_lds) return *reinterpret_cast<const u32x4 *>(sm.x + ((size_t)(f * 4 + g) * p.T + t) * 16);
+    if constexpr (XL) return *reinterpret_cast<const u32x4 *>(sm.x + 64 * f * p.T + (g * p.T + t) * 16);
     const int k = few_frag_k<F>(f, g);
     if (k >= p.H) return u32x4{0u, 0u, 0u, 0u};
     return *reinterpret_cast<const u32x4 *>(MOE_CHECKED(p.x + (size_t)t * p.H + k, 16, p.x, (size_t)p.T * p.H * 2));
@@ -212,7 +228,7 @@ __device__ __forceinline__ u32x4 few_x_frag(const FewArgs &p, const FewSmem &sm,
 template <int F>
 __device__ void few_stage_x(const FewArgs &p, FewSmem &sm) {
     const int nfrag = few_blocks(F, p.H) * FewBlock<F>::STEPS;
-    for (int i = threadIdx.x; i < nfrag * 4 * p.T; i += blockDim.x) {
+    for (int i = threadIdx.x; i < nfrag * 4 * p.T; i += kFewThreads) {
         const int t = i % p.T, fg = i / p.T, k = few_frag_k<F>(fg >> 2, fg & 3);
         u32x4 v = {0u, 0u, 0u, 0u};
         if (k < p.H)
@@ -222,161 +238,340 @@ __device__ void few_stage_x(const FewArgs &p, FewSmem &sm) {
     __syncthreads();
 }
 
+// Weight pieces travel from HBM to the MFMAs through a ring of register
+// chunks of CB blocks, one consumed while the others are in flight.  Within a
+// turn of the ring no branch holds a load (past the end of a row, or of the
+// work, the last block is loaded again), so the compiler's waits can count the
+// loads and leave the ring full; the last turn loads nothing.
+template <int F>
+struct FewRing {
+    static constexpr int CB = F == kFewBf16 ? 6 : 3;      // blocks of a chunk
+    static constexpr int GU = F == kFewBf16 ? 3 : 4;      // chunks in the gate/up's ring
+    static constexpr int DN = 4, DH = 2;                  // in the down's: weights, h
+};
+
 // Units u0 .. u1 - 1 of eight h columns: the MFMA's rows are the unit's eight
 // gate rows and the matching eight up rows; the waves split K.
-template <int F>
-__device__ void few_gateup(const FewArgs &p, FewSmem &sm, bool shared, bool in_lds, int u0, int u1) {
-    constexpr int STEPS = FewBlock<F>::STEPS;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
-    const int I = shared ? p.I_sh : p.I, H = p.H;
+template <int F, bool XL>
+__device__ __forceinline__ void few_gateup(const FewArgs &p, FewSmem &sm, bool shared, int u0, int u1) {
+    constexpr int STEPS = FewBlock<F>::STEPS, CB = FewRing<F>::CB, N = FewRing<F>::GU;
+    if (u0 >= u1) return;
+    const int lane = threadIdx.x & 63, wave = wave_index(), r = lane & 15, g = lane >> 4;
+    const int I = shared ? p.I_sh : p.I, H = p.H, per = I / 8;
     const int nb = few_blocks(F, H), b0 = wave * nb / kFewWaves, b1 = (wave + 1) * nb / kFewWaves;
+    const int nch = ((nb + kFewWaves - 1) / kFewWaves + CB - 1) / CB;   // chunks of a unit, in every wave
     const size_t pitch = F == kFewBf16 ? (size_t)H * 2 : (size_t)H / 2, spitch = F == kFewMx ? H / 32 : H / 16;
     const uint8_t *w = shared ? p.swgu : p.wgu, *s = shared ? p.sgus : p.gus;
     [[maybe_unused]] const size_t rows = (size_t)(shared ? 1 : p.E) * 2 * I;
-    for (int u = u0; u < u1; ++u) {
-        const int ue = u / (I / 8), c0 = (u - ue * (I / 8)) * 8;
-        const int e = shared ? 0 : sm.expert[ue];
-        const size_t row = (size_t)e * 2 * I + (r < 8 ? c0 + r : I + c0 + r - 8);
-        const uint8_t *wrow = w + row * pitch, *srow = s + row * spitch;
-        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-        for (int b = b0; b < b1; ++b) {
-            const u32x4 c = __builtin_nontemporal_load(
-                reinterpret_cast<const u32x4 *>(MOE_CHECKED(wrow + few_piece<F>(b, g, H), 16, w, rows * pitch)));
-            const uint32_t sc = few_scale<F>(srow, b, g, H, s, rows * spitch);
+    const size_t my_row = r < 8 ? r : I + r - 8;
+
+    // the unit being loaded: this lane's weight and scale rows, next chunk
+    int lu = u0, lch = 0, le = u0 / per, lc = u0 - le * per;
+    const int last = max(b1 - 1, 0);
+    const uint8_t *wrow, *srow;
+    auto point = [&]() {
+        const size_t row = (size_t)(shared ? 0 : uniform(sm.expert[le])) * 2 * I + 8 * lc + my_row;
+        wrow = w + row * pitch;
+        srow = s + row * spitch;
+    };
+    u32x4 c[N][CB];
+    uint32_t sc[N][CB];
+    auto load = [&](int i) {
 #pragma unroll
-            for (int i = 0; i < STEPS; ++i)
-                acc = mfma16x16x32(few_operand<F>(c, sc, i), few_x_frag<F>(p, sm, in_lds, b * STEPS + i, r, g), acc);
+        for (int j = 0; j < CB; ++j) {
+            const int b = min(b0 + lch * CB + j, last);
+            c[i][j] = __builtin_nontemporal_load(
+                reinterpret_cast<const u32x4 *>(MOE_CHECKED(wrow + few_piece<F>(b, g, H), 16, w, rows * pitch)));
+            if constexpr (F != kFewBf16) sc[i][j] = few_scale<F>(srow, b, g, H, s, rows * spitch);
         }
-        f32x4(*red)[64] = sm.red[u & 1];
+        if (lch + 1 < nch) {
+            ++lch;
+        } else if (lu + 1 < u1) {
+            lch = 0;
+            ++lu;
+            if (++lc == per) {
+                lc = 0;
+                ++le;
+            }
+            point();
+        }
+    };
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    int cu = u0, cch = 0, ce = le, cc = lc;   // the unit being summed
+    auto finish = [&]() {
+        f32x4(*red)[64] = sm.red[cu & 1];
         red[wave][lane] = acc;
-        few_lds_barrier();
+        acc = f32x4{0.f, 0.f, 0.f, 0.f};
+        __syncthreads();
         // lane 16 (m / 4) + t, element m % 4 of each wave's sums: weight row m, token t
-        if (threadIdx.x < 128) {
-            const int c = threadIdx.x & 7, t = threadIdx.x >> 3;
+        if (wave < 2) {
+            const int i = threadIdx.x & 7, t = threadIdx.x >> 3;
             float gate = 0.f, up = 0.f;
 #pragma unroll
             for (int v = 0; v < kFewWaves; ++v) {
-                gate += red[v][16 * (c >> 2) + t][c & 3];
-                up += red[v][16 * (2 + (c >> 2)) + t][c & 3];
+                gate += red[v][16 * (i >> 2) + t][i & 3];
+                up += red[v][16 * (2 + (i >> 2)) + t][i & 3];
             }
             if constexpr (F == kFewNv) {
-                const float m = (shared ? p.sgug : p.gug)[e];
+                const float m = shared ? p.sgug[0] : p.gug[uniform(sm.expert[ce])];
                 gate *= m;
                 up *= m;
             }
             const uint16_t hv = (uint16_t)f32_to_bf16_rne(gelu_tanh(gate) * up);
             if (t < p.T) {
                 if (shared) {
-                    *MOE_CHECKED(p.h_sh + (size_t)t * I + c0 + c, 2, p.h_sh, (size_t)p.T * I * 2) = hv;
-                } else if (const int j = sm.slot[ue][t]) {
-                    *MOE_CHECKED(p.h + ((size_t)t * p.k + j - 1) * I + c0 + c, 2, p.h, (size_t)p.T * p.k * I * 2) = hv;
+                    *MOE_CHECKED(p.h_sh + (size_t)t * I + 8 * cc + i, 2, p.h_sh, (size_t)p.T * I * 2) = hv;
+                } else if (const int j = sm.slot[ce][t]) {
+                    *MOE_CHECKED(p.h + ((size_t)t * p.k + j - 1) * I + 8 * cc + i, 2, p.h, (size_t)p.T * p.k * I * 2) = hv;
                 }
             }
         }
-    }
-    publish(p.ctr + kCtrGateUp);
+        if (++cc == per) {
+            cc = 0;
+            ++ce;
+        }
+    };
+    point();
+#pragma unroll
+    for (int i = 0; i < N; ++i) load(i);
+    auto turn = [&](auto more) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+#pragma unroll
+            for (int j = 0; j < CB; ++j) {
+                const int b = b0 + cch * CB + j;
+                if (uniform(b < b1))
+#pragma unroll
+                    for (int q = 0; q < STEPS; ++q)
+                        acc = mfma16x16x32(few_operand<F>(c[i][j], F == kFewBf16 ? 0u : sc[i][j], q),
+                                           few_x_frag<F, XL>(p, sm, b * STEPS + q, r, g), acc);
+            }
+            if constexpr (decltype(more)::value) load(i);
+            if (++cch == nch) {
+                if (cu < u1) finish();
+                cch = 0;
+                ++cu;
+            }
+        }
+    };
+    for (int left = ((u1 - u0) * nch - 1) / N; left > 0; --left) turn(std::true_type{});
+    turn(std::false_type{});
 }
 
 // ---------------------------------------------------------------- down
-// Sixteen output columns: the waves take the touched experts in turn (the
-// dense MLP in pieces of about an expert's size), and their sums are added in
-// wave order.
+// Sixteen output columns per item: the waves take the touched experts in turn
+// (the dense MLP in pieces of about an expert's size), and their sums are
+// added in wave order.  The ring's first weights are requested before h
+// exists; h (from L2) has a ring of its own.  A lane whose token is not routed
+// to the expert multiplies another token's row, whose sums it leaves out.
 template <int F>
-__device__ void few_down(const FewArgs &p, FewSmem &sm, int item) {
-    constexpr int STEPS = FewBlock<F>::STEPS, KB = FewBlock<F>::K;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
-    const int U = sm.n_experts;
-    const int pb = few_blocks(F, p.I), np = p.I_sh ? (few_blocks(F, p.I_sh) + pb - 1) / pb : 0;   // blocks of a piece, pieces
-    f32x4 out = {0.f, 0.f, 0.f, 0.f};
-    for (int v = wave; v < U + np; v += kFewWaves) {
-        const bool shared = v >= U;
-        const int I = shared ? p.I_sh : p.I, e = shared ? 0 : sm.expert[v], nb = few_blocks(F, I);
-        const int b0 = shared ? (v - U) * pb : 0, b1 = shared ? min(nb, b0 + pb) : nb;
-        const size_t pitch = F == kFewBf16 ? (size_t)I * 2 : (size_t)I / 2, spitch = F == kFewMx ? I / 32 : I / 16;
-        const uint8_t *w = shared ? p.swd : p.wd, *s = shared ? p.sds : p.ds;
-        const size_t row = (size_t)e * p.H + 16 * item + r;
-        [[maybe_unused]] const size_t rows = (size_t)(shared ? 1 : p.E) * p.H;
-        const uint8_t *wrow = w + row * pitch, *srow = s + row * spitch;
-        const int j = shared ? 1 : sm.slot[v][r];             // lane (r, g)'s token r: its slot + 1
-        const bool on = r < p.T && j;
-        const uint16_t *hb = shared ? p.h_sh : p.h;
-        const uint16_t *hrow = hb + (on ? (shared ? (size_t)r : (size_t)r * p.k + j - 1) * I : 0);
-        [[maybe_unused]] const size_t hbytes = (size_t)p.T * (shared ? 1 : p.k) * I * 2;
-        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-        for (int b = b0; b < b1; ++b) {
-            const u32x4 c = __builtin_nontemporal_load(
-                reinterpret_cast<const u32x4 *>(MOE_CHECKED(wrow + few_piece<F>(b, g, I), 16, w, rows * pitch)));
-            const uint32_t sc = few_scale<F>(srow, b, g, I, s, rows * spitch);
+__device__ __forceinline__ void few_down_items(const FewArgs &p, FewSmem &sm, int item) {
+    constexpr int STEPS = FewBlock<F>::STEPS, CB = FewRing<F>::CB, N = FewRing<F>::DN, M = FewRing<F>::DH;
+    const int lane = threadIdx.x & 63, wave = wave_index(), r = lane & 15, g = lane >> 4;
+    const int U = uniform(sm.n_experts), pb = few_blocks(F, p.I);
+    const int n = U + (p.I_sh ? (few_blocks(F, p.I_sh) + pb - 1) / pb : 0);   // sub-units: experts, pieces of the dense MLP
+    // blocks [b0, b1) of sub-unit v, whose rows are `width` values
+    auto span = [&](int v, int &b0, int &b1, int &width) {
+        width = v < U ? p.I : p.I_sh;
+        b0 = v < U ? 0 : (v - U) * pb;
+        b1 = min(few_blocks(F, width), b0 + pb);
+    };
+    // slot + 1 of this lane's token in sub-unit v (0: not routed there)
+    auto route = [&](int v) -> int { return r < p.T ? (v >= U ? 1 : (int)sm.slot[v][r]) : 0; };
+
+    u32x4 c[N][CB], h[M][CB][STEPS];
+    uint32_t sc[N][CB];
+    // the sub-unit whose weights are being loaded: its next block, its end
+    int lv = 0, lb = 0, lb1 = 0, lI = 0;
+    const uint8_t *wrow = nullptr, *srow = nullptr;
+    [[maybe_unused]] const uint8_t *wbase = nullptr, *sbase = nullptr;
+    [[maybe_unused]] size_t wbytes = 0, sbytes = 0;
+    auto point = [&]() {
+        const bool shared = lv >= U;
+        span(lv, lb, lb1, lI);
+        const size_t row = (size_t)(shared ? 0 : uniform(sm.expert[lv])) * p.H + 16 * item + r;
+        const size_t pitch = F == kFewBf16 ? (size_t)lI * 2 : (size_t)lI / 2, spitch = F == kFewMx ? lI / 32 : lI / 16;
+        wbase = shared ? p.swd : p.wd;
+        sbase = shared ? p.sds : p.ds;
+        wbytes = (size_t)(shared ? 1 : p.E) * p.H * pitch;
+        sbytes = (size_t)(shared ? 1 : p.E) * p.H * spitch;
+        wrow = wbase + row * pitch;
+        srow = sbase + row * spitch;
+    };
+    auto load = [&](int i) {
 #pragma unroll
-            for (int i = 0; i < STEPS; ++i) {
-                const int k = few_frag_k<F>(b * STEPS + i, g);
-                u32x4 hv = {0u, 0u, 0u, 0u};
-                if (on && (KB == 32 || k < I))
-                    hv = *reinterpret_cast<const u32x4 *>(MOE_CHECKED(hrow + k, 16, hb, hbytes));
-                acc = mfma16x16x32(few_operand<F>(c, sc, i), hv, acc);
+        for (int j = 0; j < CB; ++j) {
+            const int b = min(lb + j, lb1 - 1);
+            c[i][j] = __builtin_nontemporal_load(
+                reinterpret_cast<const u32x4 *>(MOE_CHECKED(wrow + few_piece<F>(b, g, lI), 16, wbase, wbytes)));
+            if constexpr (F != kFewBf16) sc[i][j] = few_scale<F>(srow, b, g, lI, sbase, sbytes);
+        }
+        if (lb + CB < lb1) {
+            lb += CB;
+        } else if (lv + kFewWaves < n) {
+            lv += kFewWaves;
+            point();
+        }
+    };
+    auto start = [&]() {
+        lv = wave;
+        if (lv >= n) return;
+        point();
+#pragma unroll
+        for (int i = 0; i < N; ++i) load(i);
+    };
+    // the sub-unit whose h is being loaded, and this lane's h row (where its
+    // token is not routed there, the row of one that is)
+    int hv = 0, hb = 0, hb1 = 0, hI = 0;
+    const uint16_t *hrow = nullptr;
+    [[maybe_unused]] const uint16_t *hbase = nullptr;
+    [[maybe_unused]] size_t hbytes = 0;
+    auto point_h = [&]() {
+        const bool shared = hv >= U;
+        span(hv, hb, hb1, hI);
+        const int j = route(hv), mine = shared ? r : r * p.k + j - 1;
+        const int other = __builtin_amdgcn_readlane(mine, (int)__builtin_ctzll(__ballot(j != 0) | (1ull << 63)));
+        hbase = shared ? p.h_sh : p.h;
+        hbytes = (size_t)p.T * (shared ? 1 : p.k) * hI * 2;
+        hrow = hbase + (size_t)(j ? mine : other) * hI;
+    };
+    auto load_h = [&](int i) {
+#pragma unroll
+        for (int j = 0; j < CB; ++j) {
+            const int b = min(hb + j, hb1 - 1);
+#pragma unroll
+            for (int q = 0; q < STEPS; ++q) {
+                const int k = few_frag_k<F>(b * STEPS + q, g);
+                h[i][j][q] = *reinterpret_cast<const u32x4 *>(MOE_CHECKED(hrow + (k < hI ? k : 0), 16, hbase, hbytes));
             }
         }
-        float f = shared ? 1.f : sm.w[on ? r * p.k + j - 1 : 0];
-        if constexpr (F == kFewNv) f *= (shared ? p.sdg : p.dg)[e];
-        if (on)
+        if (hb + CB < hb1) {
+            hb += CB;
+        } else if (hv + kFewWaves < n) {
+            hv += kFewWaves;
+            point_h();
+        }
+    };
+
+    for (bool have_h = false;;) {
+        // wave 0 polls for h, and loads return in order: its weights only after that
+        if (wave != 0) start();
+        if (threadIdx.x == 0) {
+            if (!have_h) wait_count(p.ctr + kCtrGateUp, p.n_gu);
+            sm.down = (int)ctr_add(p.ctr + kCtrDownTicket);
+        }
+        have_h = true;
+        __syncthreads();
+        if (wave == 0) start();
+        const int next = uniform(sm.down);
+        f32x4 out = {0.f, 0.f, 0.f, 0.f};
+        if (wave < n) {
+            hv = wave;
+            point_h();
 #pragma unroll
-            for (int q = 0; q < 4; ++q) out[q] = fmaf(f, acc[q], out[q]);
-    }
-    sm.red[0][wave][lane] = out;
-    __syncthreads();
-    if (threadIdx.x < 256) {
-        const int m = threadIdx.x & 15, t = threadIdx.x >> 4;
-        float sum = 0.f;
+            for (int i = 0; i < M; ++i) load_h(i);
+            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+            int cv = wave, cb, cb1, cI;
+            span(cv, cb, cb1, cI);
+            auto turn = [&](auto more) {
 #pragma unroll
-        for (int v = 0; v < kFewWaves; ++v) sum += sm.red[0][v][16 * (m >> 2) + t][m & 3];
-        if (t < p.T)
-            *MOE_CHECKED(p.out + (size_t)t * p.H + 16 * item + m, 2, p.out, (size_t)p.T * p.H * 2) =
-                (uint16_t)f32_to_bf16_rne(sum);
+                for (int i = 0; i < N; ++i) {
+#pragma unroll
+                    for (int j = 0; j < CB; ++j) {
+                        if (uniform(cb + j < cb1)) {
+                            u32x4 cw = c[i][j];
+                            if constexpr (F != kFewBf16) {
+                                // codes past the row (the last block of an odd number of half blocks) count as zero
+                                if (128 * (cb + j) + 32 * g >= cI) cw = u32x4{0u, 0u, 0u, 0u};
+                            }
+#pragma unroll
+                            for (int q = 0; q < STEPS; ++q)
+                                acc = mfma16x16x32(few_operand<F>(cw, F == kFewBf16 ? 0u : sc[i][j], q), h[i % M][j][q], acc);
+                        }
+                    }
+                    if constexpr (decltype(more)::value) load(i);
+                    if (decltype(more)::value || i + M < N) load_h(i % M);
+                    cb += CB;
+                    if (cb >= cb1 && cv < n) {
+                        const int j = route(cv);
+                        float f = cv >= U ? 1.f : sm.w[j ? r * p.k + j - 1 : 0];
+                        if constexpr (F == kFewNv) f *= cv >= U ? p.sdg[0] : p.dg[uniform(sm.expert[cv])];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) out[q] = j ? fmaf(f, acc[q], out[q]) : out[q];
+                        acc = f32x4{0.f, 0.f, 0.f, 0.f};
+                        cv += kFewWaves;
+                        if (cv < n) span(cv, cb, cb1, cI);
+                    }
+                }
+            };
+            int chunks = 0;
+            for (int v = wave; v < n; v += kFewWaves) {
+                int v0, v1, vI;
+                span(v, v0, v1, vI);
+                chunks += (v1 - v0 + CB - 1) / CB;
+            }
+            for (int left = (chunks - 1) / N; left > 0; --left) turn(std::true_type{});
+            turn(std::false_type{});
+        }
+        sm.red[0][wave][lane] = out;
+        __syncthreads();
+        if (threadIdx.x < 256) {
+            const int m = threadIdx.x & 15, t = threadIdx.x >> 4;
+            float sum = 0.f;
+#pragma unroll
+            for (int v = 0; v < kFewWaves; ++v) sum += sm.red[0][v][16 * (m >> 2) + t][m & 3];
+            if (t < p.T)
+                *MOE_CHECKED(p.out + (size_t)t * p.H + 16 * item + m, 2, p.out, (size_t)p.T * p.H * 2) =
+                    (uint16_t)f32_to_bf16_rne(sum);
+        }
+        __syncthreads();   // the sums and the ticket in LDS are free
+        item = next;
+        if ((uint32_t)item >= (uint32_t)p.n_down) return;
     }
 }
 
-template <int F>
-__global__ __launch_bounds__(64 * kFewWaves) void few_layer_kernel(FewArgs p) {
+// XL: the token rows fit the LDS.
+template <int F, bool XL>
+__global__ __launch_bounds__(kFewThreads) void few_layer_kernel(FewArgs p) {
     __shared__ FewSmem sm;
-    const int n1 = p.n_router, n2 = n1 + p.n_gu_sh, n3 = n2 + p.n_gu, n4 = n3 + p.n_down;
-    const bool in_lds = (size_t)few_blocks(F, p.H) * FewBlock<F>::K * 2 * p.T <= kFewXBytes;
-    bool staged = false, selected = false, have_h = false;
+    const int wave = wave_index();
+    // tickets: a router item (then more, while there are any), then a gate/up
+    // share and a down item together
+    if (threadIdx.x == 0) sm.ticket = (int)ctr_add(p.ctr + kCtrRouterTicket);
+    __syncthreads();
+    for (int t = uniform(sm.ticket); (uint32_t)t < (uint32_t)p.n_router;) {
+        few_router(p, sm, t);
+        t = publish_and_next(p.ctr + kCtrRouter, p.ctr + kCtrRouterTicket, &sm.ticket);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        const uint32_t a = ctr_add(p.ctr + kCtrGateUpTicket), b = ctr_add(p.ctr + kCtrDownTicket);
+        sm.ticket = (int)a;
+        sm.down = (int)b;
+    }
+    if constexpr (XL) few_stage_x<F>(p, sm);
+    __syncthreads();
+    int t = uniform(sm.ticket), d = uniform(sm.down);
+    bool selected = false;
     for (;;) {
-        __syncthreads();   // the LDS of the previous item is free
-        if (threadIdx.x == 0) sm.ticket = (int)ctr_add(p.ctr + kCtrTicket);
-        __syncthreads();
-        const int t = sm.ticket;
-        if (t >= n4 || t < 0) break;
-        if (t < n1) {
-            few_router(p, sm, t);
-            continue;
+        const bool share = (uint32_t)t < (uint32_t)p.n_gu;
+        if (share && p.I_sh) {
+            const int units = p.I_sh / 8;
+            few_gateup<F, XL>(p, sm, true, share_start(t, units, p.n_gu), share_start(t + 1, units, p.n_gu));
         }
-        if (t < n3 && !staged && in_lds) {
-            few_stage_x<F>(p, sm);
-            staged = true;
-        }
-        if (t >= n2 && !selected) {
-            few_select(p, sm, t == n2);
+        if (!selected) {
+            few_select(p, sm, t == 0);
             selected = true;
         }
-        if (t < n3) {
-            const bool shared = t < n2;
-            const int i = shared ? t - n1 : t - n2, n = shared ? p.n_gu_sh : p.n_gu;
-            const int units = shared ? p.I_sh / 8 : sm.n_experts * (p.I / 8);
-            few_gateup<F>(p, sm, shared, in_lds, (int)((long long)i * units / n), (int)((long long)(i + 1) * units / n));
-            continue;
-        }
-        if (!have_h) {
-            wait_for(p.ctr + kCtrGateUp, p.n_gu_sh + p.n_gu);
-            have_h = true;
-        }
-        few_down<F>(p, sm, t - n3);
+        if (!share) break;
+        const int units = uniform(sm.n_experts) * (p.I / 8);
+        few_gateup<F, XL>(p, sm, false, share_start(t, units, p.n_gu), share_start(t + 1, units, p.n_gu));
+        t = publish_and_next(p.ctr + kCtrGateUp, p.ctr + kCtrGateUpTicket, &sm.ticket);
     }
+    if ((uint32_t)d < (uint32_t)p.n_down) few_down_items<F>(p, sm, d);
     // the last workgroup to leave clears the counters for the next call
     if (threadIdx.x == 0 && ctr_add(p.ctr + kCtrExit) == gridDim.x - 1) {
-        const int all[4] = {kCtrTicket, kCtrRouter, kCtrGateUp, kCtrExit};
+        const int all[6] = {kCtrRouterTicket, kCtrGateUpTicket, kCtrDownTicket, kCtrRouter, kCtrGateUp, kCtrExit};
         for (int c : all) __hip_atomic_store(p.ctr + c, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
 }
@@ -417,14 +612,23 @@ hipError_t launch_few_layer(const FewLayer &l, hipStream_t st) {
     constexpr int kBlocks = 256;
     const long long units = (long long)std::min(l.E, l.T * l.k) * (l.I / 8);   // at most
     p.n_router = (l.E + 3) / 4;
-    p.n_gu_sh = l.I_sh ? std::min(kBlocks, l.I_sh / 8) : 0;
-    p.n_gu = (int)std::min<long long>(kBlocks, units);
+    p.n_gu = (int)std::min<long long>(kBlocks, std::max<long long>(units, l.I_sh / 8));
     p.n_down = l.H / 16;
-    const int blocks = std::min(kBlocks, std::max(std::max(p.n_router, p.n_gu), std::max(p.n_gu_sh, p.n_down)));
+    const int blocks = std::min(kBlocks, std::max(p.n_router, std::max(p.n_gu, p.n_down)));
+    const dim3 grid(blocks), block(kFewThreads);
+    const bool fits = ((size_t)l.H + 127) / 128 * 256 * l.T <= kFewXBytes;
     switch (l.fmt) {
-        case WeightFormat::kBF16: few_layer_kernel<kFewBf16><<<blocks, 64 * kFewWaves, 0, st>>>(p); break;
-        case WeightFormat::kMXFP4: few_layer_kernel<kFewMx><<<blocks, 64 * kFewWaves, 0, st>>>(p); break;
-        default: few_layer_kernel<kFewNv><<<blocks, 64 * kFewWaves, 0, st>>>(p); break;
+        case WeightFormat::kBF16:
+            if (fits) few_layer_kernel<kFewBf16, true><<<grid, block, 0, st>>>(p);
+            else few_layer_kernel<kFewBf16, false><<<grid, block, 0, st>>>(p);
+            break;
+        case WeightFormat::kMXFP4:
+            if (fits) few_layer_kernel<kFewMx, true><<<grid, block, 0, st>>>(p);
+            else few_layer_kernel<kFewMx, false><<<grid, block, 0, st>>>(p);
+            break;
+        default:
+            if (fits) few_layer_kernel<kFewNv, true><<<grid, block, 0, st>>>(p);
+            else few_layer_kernel<kFewNv, false><<<grid, block, 0, st>>>(p);
     }
     return hipGetLastError();
 }

@@ -23,6 +23,12 @@ enum FewFmt { kFewBf16 = 0, kFewMx = 1, kFewNv = 2, kFewI4 = 3 };
 
 constexpr int kFewTokens = 16;   // MFMA columns
 
+// A value that is the same in all lanes, and known to be.  Every branch around
+// an MFMA depends on such a value: MFMAs ignore the lane mask, so a branch
+// that the compiler turned into a mask would not keep them from running.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int wave_index() { return uniform(threadIdx.x >> 6); }
+
 template <int F>
 struct FewBlock {
     static constexpr int K = F == kFewBf16 ? 32 : 128;   // K values of one load
@@ -101,12 +107,6 @@ __device__ __forceinline__ void few_transpose(u32x4 &c) {
 __device__ __forceinline__ u32x4 few_i4_operand(uint32_t w) {
     constexpr uint32_t mask = 0x00780078u, base = 0x41804180u;
     return u32x4{((w << 3) & mask) | base, ((w >> 1) & mask) | base, ((w >> 5) & mask) | base, ((w >> 9) & mask) | base};
-}
-
-// Waits for this wave's LDS accesses and joins the block's barrier, leaving
-// global loads in flight (a __syncthreads may wait for them).
-__device__ __forceinline__ void few_lds_barrier() {
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
 }  // namespace moe

@@ -23,7 +23,7 @@ namespace moe {
 
 namespace {
 
-constexpr int kGemvWaves = 8;
+constexpr int kGemvWaves = 8, kGemvThreads = 64 * kGemvWaves;
 constexpr int kGemvXBytes = 128 * 1024;
 constexpr int kGemvBlocks = 256;    // a workgroup per CU
 
@@ -83,10 +83,10 @@ __device__ __forceinline__ void gemv_store(const GemvArgs &p, int u, int m, int 
 }
 
 template <int F, int GROUP>
-__global__ __launch_bounds__(64 * kGemvWaves) void gemv_w4_kernel(GemvArgs p) {
+__global__ __launch_bounds__(kGemvThreads) void gemv_w4_kernel(GemvArgs p) {
     __shared__ GemvSmem sm;
     constexpr int STEPS = FewBlock<F>::STEPS;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
+    const int lane = threadIdx.x & 63, wave = wave_index(), r = lane & 15, g = lane >> 4;
     const int range = blockIdx.x / p.slices, slice = blockIdx.x % p.slices;
     const int nb = few_blocks(F, p.K);
     const int s0 = (int)((long long)slice * nb / p.slices), s1 = (int)((long long)(slice + 1) * nb / p.slices);
@@ -95,7 +95,7 @@ __global__ __launch_bounds__(64 * kGemvWaves) void gemv_w4_kernel(GemvArgs p) {
     [[maybe_unused]] const size_t xbytes = (size_t)((T - 1) * p.ldx + K) * 2;
 
     // token rows of this K range, zero past K
-    for (int i = threadIdx.x; i < (s1 - s0) * STEPS * 4 * T; i += blockDim.x) {
+    for (int i = threadIdx.x; i < (s1 - s0) * STEPS * 4 * T; i += kGemvThreads) {
         const int t = i % T, fg = i / T, k = few_frag_k<F>(s0 * STEPS + (fg >> 2), fg & 3);
         u32x4 v = {0u, 0u, 0u, 0u};
         if (k < K) v = *reinterpret_cast<const u32x4 *>(MOE_CHECKED(p.x + t * p.ldx + k, 16, p.x, xbytes));
@@ -104,7 +104,7 @@ __global__ __launch_bounds__(64 * kGemvWaves) void gemv_w4_kernel(GemvArgs p) {
     __syncthreads();
     if constexpr (F == kFewI4) {
         const int per = GROUP / 8;   // 16-byte pieces of one group and token, at stride 16 T
-        for (int i = threadIdx.x; i < (s1 - s0) * (128 / GROUP) * T; i += blockDim.x) {
+        for (int i = threadIdx.x; i < (s1 - s0) * (128 / GROUP) * T; i += kGemvThreads) {
             const int t = i % T, grp = i / T;
             float s = 0.f;
             for (int j = 0; j < per; ++j) {
@@ -165,7 +165,7 @@ __global__ __launch_bounds__(64 * kGemvWaves) void gemv_w4_kernel(GemvArgs p) {
         }
         f32x4(*red)[64] = sm.red[u & 1];
         red[wave][lane] = acc;
-        few_lds_barrier();
+        __syncthreads();
         // lane 16 (m / 4) + t, element m % 4 of each wave's sums: weight row m, token t
         if (threadIdx.x < 256) {
             const int m = threadIdx.x & 15, t = threadIdx.x >> 4;
@@ -243,7 +243,7 @@ hipError_t launch_gemv_w4(const GemvW4 &l, hipStream_t st) {
     p.slices = g.slices;
     p.geglu = l.geglu;
     p.y_fp32 = l.y_fp32;
-    const dim3 grid(g.ranges * g.slices), block(64 * kGemvWaves);
+    const dim3 grid(g.ranges * g.slices), block(kGemvThreads);
     if (l.fmt == GemvFormat::kMXFP4) gemv_w4_kernel<kFewMx, 0><<<grid, block, 0, st>>>(p);
     else if (l.fmt == GemvFormat::kNVFP4) gemv_w4_kernel<kFewNv, 0><<<grid, block, 0, st>>>(p);
     else if (l.group == 32) gemv_w4_kernel<kFewI4, 32><<<grid, block, 0, st>>>(p);

@@ -124,7 +124,7 @@ struct FewLayer {
     uint16_t *h, *h_sh;      // [T*k][I], [T][I_sh]
     int T, H, E, k, I, I_sh;
 };
-constexpr int kFewCounterBytes = 512;
+constexpr int kFewCounterBytes = 1024;
 hipError_t launch_few_layer(const FewLayer &l, hipStream_t st);
 
 // Matrix-vector products with 4-bit weights for up to kFewMaxT tokens.
