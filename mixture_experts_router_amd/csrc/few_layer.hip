@@ -32,7 +32,8 @@ namespace moe {
 namespace {
 
 constexpr int kFewWaves = 8, kFewThreads = 64 * kFewWaves;
-constexpr int kFewXBytes = 128 * 1024;                    // token rows in LDS
+constexpr int kFewXBytes = 96 * 1024;                     // token rows in LDS
+constexpr int kFewBatch = 4;                              // gate/up units reduced together
 constexpr int kFewMaxA = kFewTokens * 32;                 // assignments (k <= 32)
 
 // Counters in the workspace's zeroed prefix, a line each.
@@ -58,7 +59,7 @@ struct FewArgs {
 
 struct FewSmem {
     uint8_t x[kFewXBytes];                      // token operands, in MFMA order
-    f32x4 red[2][kFewWaves][64];                // partial sums of the waves
+    f32x4 red[kFewBatch][kFewWaves][64];        // partial sums of the waves
     int32_t ids[kFewMaxA];
     float w[kFewMaxA];
     uint8_t slot[kFewMaxA][kFewTokens];         // [touched expert][token]: slot + 1, 0 = not routed there
@@ -73,26 +74,25 @@ __device__ __forceinline__ uint32_t ctr_add(uint32_t *p) {
     return __hip_atomic_fetch_add(p, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// Publishes what this workgroup has written (every wave's stores are complete,
-// then one thread makes them visible device-wide and counts) and takes the
-// next ticket of the phase.  Both happen in one branch of thread 0, and
-// barriers stand on either side of it: two such branches with no barrier
-// between them, as at the end and the start of a loop's body, may be joined by
-// the compiler across the back edge, which lets the other lanes run ahead.
-__device__ __forceinline__ int publish_and_next(uint32_t *done, uint32_t *tickets, int *slot) {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        __threadfence();
-        ctr_add(done);
-        *slot = (int)ctr_add(tickets);
-    }
-    __syncthreads();
-    return uniform(*slot);
+// What one workgroup computes for others (logits, h) is stored through the
+// caches, at agent scope, so that publishing it takes no cache write-back (a
+// write-back by every workgroup cost 4 us a phase): once a store is complete,
+// every workgroup that loads the line for the first time sees it.
+template <typename V>
+__device__ __forceinline__ void store_shared(V *p, V v) {
+    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// One thread waits until `n` workgroups have published, and makes what they
-// wrote visible to its workgroup, which joins a barrier next: the caches'
+// Counts this workgroup's stored results: every wave's stores are complete,
+// then one thread counts.
+__device__ __forceinline__ void publish(uint32_t *done) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (threadIdx.x == 0) ctr_add(done);
+}
+
+// One thread waits until `n` workgroups have published; its workgroup, which
+// joins a barrier next, may then load what they stored: the caches'
 // invalidation is complete, not merely requested, before the others load.
 // The count is reached as long as the counters were zero before the launch;
 // the bound only keeps a workspace that was not from holding the GPU (its
@@ -102,7 +102,7 @@ __device__ __forceinline__ void wait_count(uint32_t *ctr, uint32_t n) {
         if (__hip_atomic_load(ctr, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) >= n) break;
         __builtin_amdgcn_s_sleep(1);
     }
-    __threadfence();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
@@ -124,24 +124,32 @@ __device__ void few_router(const FewArgs &p, FewSmem &sm, int item) {
     const int et = threadIdx.x >> 4, tt = threadIdx.x & 15;                       // of the adding threads (< 64)
     double total = 0.0;
     for (int c0 = 0; c0 < nchunks; c0 += 2 * kFewWaves) {
-        for (int cc = wave; cc < 2 * kFewWaves && c0 + cc < nchunks; cc += kFewWaves) {
-            const int k0 = (c0 + cc) * 256, n = min(256, p.H - k0) / 32;
-            u32x4 a[8], b[8];
+        // this wave's two chunks, c0 + wave and c0 + wave + 8: all their loads go out at once
+        u32x4 a[2][8], b[2][8];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int k0 = min(c0 + wave + i * kFewWaves, nchunks - 1) * 256, n = min(256, p.H - k0) / 32;
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
                 const int k = k0 + 32 * (u < n ? u : 0) + 8 * g;
-                a[u] = on_e ? *reinterpret_cast<const u32x4 *>(
-                                  MOE_CHECKED(p.wr + (size_t)(e0 + r) * p.H + k, 16, p.wr, (size_t)p.E * p.H * 2))
-                            : u32x4{0u, 0u, 0u, 0u};
-                b[u] = on_t ? *reinterpret_cast<const u32x4 *>(
-                                  MOE_CHECKED(p.x + (size_t)r * p.H + k, 16, p.x, (size_t)p.T * p.H * 2))
-                            : u32x4{0u, 0u, 0u, 0u};
+                a[i][u] = on_e ? *reinterpret_cast<const u32x4 *>(
+                                     MOE_CHECKED(p.wr + (size_t)(e0 + r) * p.H + k, 16, p.wr, (size_t)p.E * p.H * 2))
+                               : u32x4{0u, 0u, 0u, 0u};
+                b[i][u] = on_t ? *reinterpret_cast<const u32x4 *>(
+                                     MOE_CHECKED(p.x + (size_t)r * p.H + k, 16, p.x, (size_t)p.T * p.H * 2))
+                               : u32x4{0u, 0u, 0u, 0u};
             }
-            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+        }
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-                if (u < n) acc = mfma16x16x32(a[u], b[u], acc);
-            if (g == 0) sum[cc][r] = acc;
+        for (int i = 0; i < 2; ++i) {
+            const int cc = wave + i * kFewWaves, n = min(256, p.H - (c0 + cc) * 256) / 32;
+            if (uniform(c0 + cc < nchunks)) {
+                f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    if (uniform(u < n)) acc = mfma16x16x32(a[i][u], b[i][u], acc);
+                if (g == 0) sum[cc][r] = acc;
+            }
         }
         __syncthreads();
         if (threadIdx.x < 64)
@@ -150,7 +158,8 @@ __device__ void few_router(const FewArgs &p, FewSmem &sm, int item) {
     }
     if (threadIdx.x < 64 && tt < p.T && e0 + et < p.E) {
         const double b = p.bias ? (double)p.bias[e0 + et] : 0.0;
-        *MOE_CHECKED(p.logits + (size_t)tt * p.E + e0 + et, 4, p.logits, (size_t)p.T * p.E * 4) = (float)(total + b);
+        store_shared(MOE_CHECKED(p.logits + (size_t)tt * p.E + e0 + et, 4, p.logits, (size_t)p.T * p.E * 4),
+                     (float)(total + b));
     }
 }
 
@@ -297,39 +306,45 @@ __device__ __forceinline__ void few_gateup(const FewArgs &p, FewSmem &sm, bool s
         }
     };
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-    int cu = u0, cch = 0, ce = le, cc = lc;   // the unit being summed
+    int cu = u0, cch = 0, held = 0;   // the unit being summed; units whose sums are in LDS
     auto finish = [&]() {
-        f32x4(*red)[64] = sm.red[cu & 1];
-        red[wave][lane] = acc;
+        sm.red[held][wave][lane] = acc;
         acc = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (++held < kFewBatch && cu + 1 < u1) return;
         __syncthreads();
-        // lane 16 (m / 4) + t, element m % 4 of each wave's sums: weight row m, token t
-        if (wave < 2) {
-            const int i = threadIdx.x & 7, t = threadIdx.x >> 3;
-            float gate = 0.f, up = 0.f;
+        // wave v finishes held unit v: lane 4 t + i has token t and columns 2i, 2i + 1.  Lane 16 (m / 4) + t,
+        // element m % 4 of each wave's sums is weight row m, token t: gate rows 0..7, up rows 8..15
+        if (uniform(wave < held)) {
+            const int i = 2 * (lane & 3), t = lane >> 2, u = cu + 1 - held + wave, ue = u / per;
+            float gate[2] = {0.f, 0.f}, up[2] = {0.f, 0.f};
 #pragma unroll
             for (int v = 0; v < kFewWaves; ++v) {
-                gate += red[v][16 * (i >> 2) + t][i & 3];
-                up += red[v][16 * (2 + (i >> 2)) + t][i & 3];
-            }
-            if constexpr (F == kFewNv) {
-                const float m = shared ? p.sgug[0] : p.gug[uniform(sm.expert[ce])];
-                gate *= m;
-                up *= m;
-            }
-            const uint16_t hv = (uint16_t)f32_to_bf16_rne(gelu_tanh(gate) * up);
-            if (t < p.T) {
-                if (shared) {
-                    *MOE_CHECKED(p.h_sh + (size_t)t * I + 8 * cc + i, 2, p.h_sh, (size_t)p.T * I * 2) = hv;
-                } else if (const int j = sm.slot[ce][t]) {
-                    *MOE_CHECKED(p.h + ((size_t)t * p.k + j - 1) * I + 8 * cc + i, 2, p.h, (size_t)p.T * p.k * I * 2) = hv;
+                const float *a = reinterpret_cast<const float *>(&sm.red[wave][v][16 * (i >> 2) + t]) + (i & 3);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    gate[q] += a[q];
+                    up[q] += a[4 * 32 + q];
                 }
             }
+            if constexpr (F == kFewNv) {
+                const float m = shared ? p.sgug[0] : p.gug[uniform(sm.expert[ue])];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    gate[q] *= m;
+                    up[q] *= m;
+                }
+            }
+            const uint32_t hv = pack_bf16x2(gelu_tanh(gate[0]) * up[0], gelu_tanh(gate[1]) * up[1]);
+            const int j = t < p.T ? (shared ? 1 : (int)sm.slot[ue][t]) : 0;
+            if (j) {
+                uint16_t *base = shared ? p.h_sh : p.h;
+                const size_t row = shared ? (size_t)t : (size_t)t * p.k + j - 1;
+                store_shared(reinterpret_cast<uint32_t *>(MOE_CHECKED(base + row * I + 8 * (u - ue * per) + i, 4, base,
+                                                                      (size_t)p.T * (shared ? 1 : p.k) * I * 2)), hv);
+            }
         }
-        if (++cc == per) {
-            cc = 0;
-            ++ce;
-        }
+        held = 0;
+        __syncthreads();
     };
     point();
 #pragma unroll
@@ -541,7 +556,17 @@ __global__ __launch_bounds__(kFewThreads) void few_layer_kernel(FewArgs p) {
     __syncthreads();
     for (int t = uniform(sm.ticket); (uint32_t)t < (uint32_t)p.n_router;) {
         few_router(p, sm, t);
-        t = publish_and_next(p.ctr + kCtrRouter, p.ctr + kCtrRouterTicket, &sm.ticket);
+        // (publication and the next ticket in one branch of thread 0, with barriers on either side: two such
+        // branches with no barrier between them, as at the end and the start of a loop's body, may be joined by
+        // the compiler across the back edge, which lets the other lanes run ahead)
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            ctr_add(p.ctr + kCtrRouter);
+            sm.ticket = (int)ctr_add(p.ctr + kCtrRouterTicket);
+        }
+        __syncthreads();
+        t = uniform(sm.ticket);
     }
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -551,22 +576,25 @@ __global__ __launch_bounds__(kFewThreads) void few_layer_kernel(FewArgs p) {
     }
     if constexpr (XL) few_stage_x<F>(p, sm);
     __syncthreads();
-    int t = uniform(sm.ticket), d = uniform(sm.down);
-    bool selected = false;
-    for (;;) {
-        const bool share = (uint32_t)t < (uint32_t)p.n_gu;
-        if (share && p.I_sh) {
+    int t = uniform(sm.ticket);
+    const int d = uniform(sm.down);
+    if (p.I_sh && (uint32_t)t < (uint32_t)p.n_gu) {   // needs no routing
+        const int units = p.I_sh / 8;
+        few_gateup<F, XL>(p, sm, true, share_start(t, units, p.n_gu), share_start(t + 1, units, p.n_gu));
+    }
+    few_select(p, sm, t == 0);
+    for (bool first = true; (uint32_t)t < (uint32_t)p.n_gu; first = false) {
+        // the next ticket, early: none is left unless a workgroup has not started yet
+        if (threadIdx.x == 0) sm.ticket = (int)ctr_add(p.ctr + kCtrGateUpTicket);
+        if (!first && p.I_sh) {
             const int units = p.I_sh / 8;
             few_gateup<F, XL>(p, sm, true, share_start(t, units, p.n_gu), share_start(t + 1, units, p.n_gu));
         }
-        if (!selected) {
-            few_select(p, sm, t == 0);
-            selected = true;
-        }
-        if (!share) break;
         const int units = uniform(sm.n_experts) * (p.I / 8);
         few_gateup<F, XL>(p, sm, false, share_start(t, units, p.n_gu), share_start(t + 1, units, p.n_gu));
-        t = publish_and_next(p.ctr + kCtrGateUp, p.ctr + kCtrGateUpTicket, &sm.ticket);
+        publish(p.ctr + kCtrGateUp);
+        t = uniform(sm.ticket);
+        __syncthreads();
     }
     if ((uint32_t)d < (uint32_t)p.n_down) few_down_items<F>(p, sm, d);
     // the last workgroup to leave clears the counters for the next call
