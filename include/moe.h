@@ -346,7 +346,8 @@ int moe_quantize_nv(const uint16_t *src, int64_t rows, int32_t K, const float *i
  *   weights, scales  as for moe_forward / moe_forward_shared; formats
  *                    MOE_W_BF16, MOE_W_MXFP4 and MOE_W_NVFP4 (the dense MLP
  *                    in the experts' format too, an NVFP4 one with a scale
- *                    buffer for E = 1); 4-bit codes 16-byte aligned
+ *                    buffer for E = 1); 4-bit codes 16-byte, scales 4-byte
+ *                    aligned
  *   I_sh             0 (no dense MLP: its four arguments are ignored) or a
  *                    positive multiple of 64
  *   out              [T][H] bf16 out, no overlap with the inputs
@@ -396,10 +397,11 @@ enum {
  *   x       [T][ldx] bf16, 16-byte aligned
  *   w       [N][K/2] codes, 16-byte aligned
  *   scales  MXFP4: E8M0 [N][K/32]; NVFP4: a scale buffer for E = 1 (header,
- *           then E4M3 [N][K/16]), 4-byte aligned; INT4: bf16 [N][K/group],
- *           2-byte aligned
+ *           then E4M3 [N][K/16]); INT4: bf16 [N][K/group]
  *   zeros   MOE_W_INT4: uint8 [N][K/group] or NULL (8 everywhere); otherwise
  *           NULL
+ *           (both 4-byte aligned and read in whole 4-byte words: up to 3
+ *           bytes behind the last value, in the same word, are read too)
  *   bias    [N] fp32 or NULL
  *   y       [T][ldy] out (N, or N/2 columns with GEGLU), bf16 (2-byte
  *           aligned) or fp32 (4-byte aligned); what lies between the rows is
@@ -413,8 +415,8 @@ int moe_gemv_w4(const moe_w4_shape *s, const uint16_t *x, const uint8_t *w, cons
                 const uint8_t *zeros, const float *bias, void *y, void *ws, size_t ws_bytes,
                 moe_stream_t stream);
 
-/* Workspace bytes moe_gemv_w4 needs for this shape (0: none needed, or an
- * invalid shape). */
+/* Workspace bytes moe_gemv_w4 needs for this shape, with zeros or without (0:
+ * none needed, or an invalid shape). */
 size_t moe_gemv_w4_workspace_bytes(const moe_w4_shape *s);
 
 /* Workspace bytes moe_forward needs for this shape; 0 for an invalid or

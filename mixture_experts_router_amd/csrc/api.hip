@@ -192,7 +192,8 @@ int check_few(const moe_shape *s, int32_t I_sh) {
 int check_few_weights(const moe_shape *s, const void *w, const uint8_t *scales) {
     const int st = check_weights(s, w, scales);
     if (st != MOE_OK) return st;
-    return al16(w) ? MOE_OK : MOE_ERR_INVALID_ARGUMENT;
+    // whole 16-byte pieces of the codes and aligned 4-byte words of the scales are loaded
+    return al16(w) && (!scales || al4(scales)) ? MOE_OK : MOE_ERR_INVALID_ARGUMENT;
 }
 
 moe::FewWeights few_weights(const moe_shape *s, int E, const void *w, const uint8_t *scales) {
@@ -222,9 +223,14 @@ int check_w4(const moe_w4_shape *s) {
     return MOE_OK;
 }
 
-size_t gemv_ws(const moe_w4_shape *s) {
-    const size_t part =
-        moe::gemv_part_bytes(moe::gemv_plan(s->T, s->N, s->K, s->flags & MOE_GEMV_GEGLU), s->T);
+moe::GemvFormat gemv_format(const moe_w4_shape *s) {
+    return s->w_format == MOE_W_INT4 ? moe::GemvFormat::kINT4
+                                     : (s->w_format == MOE_W_NVFP4 ? moe::GemvFormat::kNVFP4 : moe::GemvFormat::kMXFP4);
+}
+
+size_t gemv_ws(const moe_w4_shape *s, bool zeros) {
+    const size_t part = moe::gemv_part_bytes(
+        moe::gemv_plan(gemv_format(s), s->group, zeros, s->T, s->N, s->K, s->flags & MOE_GEMV_GEGLU), s->T);
     return part ? MOE_FEW_ZERO_BYTES + round_up(part) : 0;
 }
 
@@ -604,7 +610,8 @@ int moe_forward_few(const moe_shape *s, const uint16_t *x, const uint16_t *w_rou
 
 size_t moe_gemv_w4_workspace_bytes(const moe_w4_shape *s) {
     if (check_w4(s) != MOE_OK) return 0;
-    return gemv_ws(s);
+    const size_t a = gemv_ws(s, false), b = s->w_format == MOE_W_INT4 ? gemv_ws(s, true) : 0;
+    return a > b ? a : b;
 }
 
 int moe_gemv_w4(const moe_w4_shape *s, const uint16_t *x, const uint8_t *w, const uint8_t *scales,
@@ -614,10 +621,9 @@ int moe_gemv_w4(const moe_w4_shape *s, const uint16_t *x, const uint8_t *w, cons
     const bool i4 = s->w_format == MOE_W_INT4, nv = s->w_format == MOE_W_NVFP4;
     const bool y_fp32 = s->flags & MOE_GEMV_Y_FP32, geglu = s->flags & MOE_GEMV_GEGLU;
     if (!x || !w || !scales || !y || !al16(x) || !al16(w)) return MOE_ERR_INVALID_ARGUMENT;
-    if ((nv && !al4(scales)) || (i4 && (reinterpret_cast<uintptr_t>(scales) & 1u))) return MOE_ERR_INVALID_ARGUMENT;
-    if ((zeros && !i4) || (bias && !al4(bias))) return MOE_ERR_INVALID_ARGUMENT;
+    if (!al4(scales) || (zeros && (!i4 || !al4(zeros))) || (bias && !al4(bias))) return MOE_ERR_INVALID_ARGUMENT;
     if (reinterpret_cast<uintptr_t>(y) & (y_fp32 ? 3u : 1u)) return MOE_ERR_INVALID_ARGUMENT;
-    const size_t need = gemv_ws(s);
+    const size_t need = moe_gemv_w4_workspace_bytes(s);   // with or without zeros
     if (need && (!ws || ws_bytes < need || !al16(ws))) return MOE_ERR_WORKSPACE;
     moe::GemvW4 l{};
     l.x = x;
@@ -635,7 +641,7 @@ int moe_gemv_w4(const moe_w4_shape *s, const uint16_t *x, const uint8_t *w, cons
     l.N = s->N;
     l.K = s->K;
     l.group = s->group;
-    l.fmt = i4 ? moe::GemvFormat::kINT4 : (nv ? moe::GemvFormat::kNVFP4 : moe::GemvFormat::kMXFP4);
+    l.fmt = gemv_format(s);
     l.geglu = geglu;
     l.y_fp32 = y_fp32;
     return hip_status(moe::launch_gemv_w4(l, static_cast<hipStream_t>(stream)));

@@ -21,7 +21,6 @@
 // by workgroups that are running: every wait ends, whatever else runs on the
 // GPU and however few workgroups are resident.
 #include <algorithm>
-#include <type_traits>
 
 #include "few_stream.h"
 #include "moe_launch.h"
@@ -32,9 +31,8 @@ namespace moe {
 namespace {
 
 constexpr int kFewWaves = 8, kFewThreads = 64 * kFewWaves;
-constexpr int kFewXBytes = 96 * 1024;                     // token rows in LDS
-constexpr int kFewBatch = 4;                              // gate/up units reduced together
 constexpr int kFewMaxA = kFewTokens * 32;                 // assignments (k <= 32)
+constexpr int kFewArea = 136 * 1024;                      // LDS for the rings and the token rows
 
 // Counters in the workspace's zeroed prefix, a line each.
 constexpr int kCtrRouterTicket = 0, kCtrGateUpTicket = 32, kCtrDownTicket = 64;   // next item of each phase
@@ -58,13 +56,15 @@ struct FewArgs {
 };
 
 struct FewSmem {
-    uint8_t x[kFewXBytes];                      // token operands, in MFMA order
-    f32x4 red[kFewBatch][kFewWaves][64];        // partial sums of the waves
+    alignas(1024) uint8_t area[kFewArea];                     // the waves' rings, then x (gate/up) or rows of h (down)
+    f32x4 red[kFewWaves][64];                   // partial sums of the waves
     int32_t ids[kFewMaxA];
     float w[kFewMaxA];
-    uint8_t slot[kFewMaxA][kFewTokens];         // [touched expert][token]: slot + 1, 0 = not routed there
+    alignas(16) uint8_t slot[kFewMaxA][kFewTokens];   // [touched expert][token]: slot + 1, 0 = not routed there
     int16_t expert[kFewMaxA];                   // touched experts, ascending
-    int16_t index[1024];                        // expert -> touched index (or -1)
+    int16_t first[kFewMaxA + 2];                // their first position in expert order; [n_experts] = T k
+    int16_t sorted[kFewMaxA];                   // assignments in expert order
+    uint32_t mask[32];                          // touched experts
     int n_experts;
     int ticket, down;
 };
@@ -184,12 +184,24 @@ __device__ __forceinline__ void few_topk(const FewArgs &p, FewSmem &sm, int t, b
     }
 }
 
+// How many of the first n bytes of a row of `slot` are set (a byte is below 128).
+__device__ __forceinline__ int few_count(const u32x4 &row, int n) {
+    int c = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const int b = min(max(n - 4 * q, 0), 4);
+        c += __popc((row[q] + 0x7F7F7F7Fu) & 0x80808080u & (uint32_t)((1ull << (8 * b)) - 1));
+    }
+    return c;
+}
+
 // The routing of every token, by each workgroup for itself: ids and weights,
-// the touched experts in ascending order and who goes there.
+// the touched experts in ascending order, who goes there, and the assignments
+// in (expert, token) order.
 __device__ void few_select(const FewArgs &p, FewSmem &sm, bool store) {
-    const int wave = wave_index(), lane = threadIdx.x & 63, A = p.T * p.k;
-    for (int i = threadIdx.x; i < p.E; i += kFewThreads) sm.index[i] = -1;
+    const int wave = wave_index(), A = p.T * p.k, a = threadIdx.x;
     for (int i = threadIdx.x; i < A * kFewTokens / 4; i += kFewThreads) reinterpret_cast<uint32_t *>(sm.slot)[i] = 0u;
+    if (threadIdx.x < 32) sm.mask[threadIdx.x] = 0u;
     if (threadIdx.x == 0) wait_count(p.ctr + kCtrRouter, p.n_router);
     __syncthreads();
     for (int t = wave; t < p.T; t += kFewWaves) {
@@ -200,25 +212,41 @@ __device__ void few_select(const FewArgs &p, FewSmem &sm, bool store) {
         else few_topk<16>(p, sm, t, store);
     }
     __syncthreads();
-    for (int a = threadIdx.x; a < A; a += kFewThreads) sm.index[sm.ids[a]] = 0;
+    const int e = a < A ? sm.ids[a] : 0;   // thread a: assignment a (A <= the threads)
+    if (a < A) atomicOr(&sm.mask[e >> 5], 1u << (e & 31));
     __syncthreads();
-    if (wave == 0) {
-        int n = 0;
-        for (int e0 = 0; e0 < p.E; e0 += 64) {
-            const bool on = e0 + lane < p.E && sm.index[e0 + lane] >= 0;
-            const uint64_t m = __ballot(on);
-            const int at = n + __popcll(m & ((1ull << lane) - 1));
-            if (on) {
-                sm.index[e0 + lane] = (int16_t)at;
-                sm.expert[at] = (int16_t)(e0 + lane);
-            }
-            n += __popcll(m);
-        }
-        if (lane == 0) sm.n_experts = n;
+    int u = 0, n = 0;
+    for (int i = 0; i < (p.E + 31) / 32; ++i) {
+        const uint32_t m = sm.mask[i];
+        u += __popc(i < (e >> 5) ? m : i == (e >> 5) ? m & ((1u << (e & 31)) - 1) : 0u);
+        n += __popc(m);
     }
+    if (a < A) {
+        sm.slot[u][a / p.k] = (uint8_t)(a % p.k + 1);
+        sm.expert[u] = (int16_t)e;
+    }
+    if (threadIdx.x == 0) sm.n_experts = n;
     __syncthreads();
-    for (int a = threadIdx.x; a < A; a += kFewThreads)
-        sm.slot[sm.index[sm.ids[a]]][a / p.k] = (uint8_t)(a % p.k + 1);
+    // positions in expert order: a touched expert's count by each thread, then the counts before it
+    const int count = a < n ? few_count(*reinterpret_cast<const u32x4 *>(sm.slot[a]), kFewTokens) : 0;
+    // inclusive sum over the wave, then over the waves before
+    const int lane = threadIdx.x & 63;
+    int incl = count;
+    for (int d = 1; d < 64; d <<= 1) {
+        const int v = __shfl_up(incl, d);
+        if (lane >= d) incl += v;
+    }
+    int *part = reinterpret_cast<int *>(sm.red);
+    if (lane == 63) part[wave] = incl;
+    __syncthreads();
+    int at = incl - count;
+    for (int v = 0; v < wave; ++v) at += part[v];
+    if (a < n) {
+        sm.first[a] = (int16_t)at;
+        for (int t = 0; t < p.T; ++t)
+            if (const int j = sm.slot[a][t]) sm.sorted[at++] = (int16_t)(t * p.k + j - 1);
+        if (a == n - 1) sm.first[n] = (int16_t)at;
+    }
     __syncthreads();
 }
 
@@ -226,100 +254,111 @@ __device__ void few_select(const FewArgs &p, FewSmem &sm, bool store) {
 // The token operand of MFMA f, lane (r, g): from LDS, where every fragment
 // has 16 bytes per (g, token), or from the rows of x.
 template <int F, bool XL>
-__device__ __forceinline__ u32x4 few_x_frag(const FewArgs &p, const FewSmem &sm, int f, int r, int g) {
+__device__ __forceinline__ u32x4 few_x_frag(const FewArgs &p, const uint8_t *xs, int f, int r, int g) {
     const int t = min(r, p.T - 1);
-    if constexpr (XL) return *reinterpret_cast<const u32x4 *>(sm.x + 64 * f * p.T + (g * p.T + t) * 16);
+    if constexpr (XL) return *reinterpret_cast<const u32x4 *>(xs + 64 * f * p.T + (g * p.T + t) * 16);
     const int k = few_frag_k<F>(f, g);
-    if (k >= p.H) return u32x4{0u, 0u, 0u, 0u};
-    return *reinterpret_cast<const u32x4 *>(MOE_CHECKED(p.x + (size_t)t * p.H + k, 16, p.x, (size_t)p.T * p.H * 2));
+    u32x4 v = *reinterpret_cast<const u32x4 *>(
+        MOE_CHECKED(p.x + (size_t)t * p.H + (k < p.H ? k : 0), 16, p.x, (size_t)p.T * p.H * 2));
+    return k < p.H ? v : u32x4{0u, 0u, 0u, 0u};
 }
 
 template <int F>
-__device__ void few_stage_x(const FewArgs &p, FewSmem &sm) {
-    const int nfrag = few_blocks(F, p.H) * FewBlock<F>::STEPS;
+__device__ void few_stage_x(const FewArgs &p, uint8_t *xs) {
+    const int nfrag = few_steps(F, p.H) * FewStep<F>::FRAGS;
     for (int i = threadIdx.x; i < nfrag * 4 * p.T; i += kFewThreads) {
         const int t = i % p.T, fg = i / p.T, k = few_frag_k<F>(fg >> 2, fg & 3);
         u32x4 v = {0u, 0u, 0u, 0u};
         if (k < p.H)
             v = *reinterpret_cast<const u32x4 *>(MOE_CHECKED(p.x + (size_t)t * p.H + k, 16, p.x, (size_t)p.T * p.H * 2));
-        *reinterpret_cast<u32x4 *>(sm.x + (size_t)i * 16) = v;
+        *reinterpret_cast<u32x4 *>(xs + (size_t)i * 16) = v;
     }
     __syncthreads();
 }
 
-// Weight pieces travel from HBM to the MFMAs through a ring of register
-// chunks of CB blocks, one consumed while the others are in flight.  Within a
-// turn of the ring no branch holds a load (past the end of a row, or of the
-// work, the last block is loaded again), so the compiler's waits can count the
-// loads and leave the ring full; the last turn loads nothing.
-template <int F>
-struct FewRing {
-    static constexpr int CB = F == kFewBf16 ? 6 : 3;      // blocks of a chunk
-    static constexpr int GU = F == kFewBf16 ? 3 : 4;      // chunks in the gate/up's ring
-    static constexpr int DN = 4, DH = 2;                  // in the down's: weights, h
-};
-
 // Units u0 .. u1 - 1 of eight h columns: the MFMA's rows are the unit's eight
-// gate rows and the matching eight up rows; the waves split K.
-template <int F, bool XL>
+// gate rows and the matching eight up rows.  The workgroup takes 8 / KW units
+// at a time, KW waves splitting the K of each.
+template <int F, int S, bool XL>
 __device__ __forceinline__ void few_gateup(const FewArgs &p, FewSmem &sm, bool shared, int u0, int u1) {
-    constexpr int STEPS = FewBlock<F>::STEPS, CB = FewRing<F>::CB, N = FewRing<F>::GU;
-    if (u0 >= u1) return;
+    constexpr int SLOT = FewStep<F>::SLOT, OPS = FewStep<F>::OPS, FRAGS = FewStep<F>::FRAGS;
     const int lane = threadIdx.x & 63, wave = wave_index(), r = lane & 15, g = lane >> 4;
     const int I = shared ? p.I_sh : p.I, H = p.H, per = I / 8;
-    const int nb = few_blocks(F, H), b0 = wave * nb / kFewWaves, b1 = (wave + 1) * nb / kFewWaves;
-    const int nch = ((nb + kFewWaves - 1) / kFewWaves + CB - 1) / CB;   // chunks of a unit, in every wave
-    const size_t pitch = F == kFewBf16 ? (size_t)H * 2 : (size_t)H / 2, spitch = F == kFewMx ? H / 32 : H / 16;
+    if (u0 >= u1) return;
+    const int ns = few_steps(F, H), KW = few_kwaves(u1 - u0, ns), UG = kFewWaves / KW;
+    const int kw = wave % KW, s0 = kw * ns / KW, s1 = (kw + 1) * ns / KW;
     const uint8_t *w = shared ? p.swgu : p.wgu, *s = shared ? p.sgus : p.gus;
-    [[maybe_unused]] const size_t rows = (size_t)(shared ? 1 : p.E) * 2 * I;
-    const size_t my_row = r < 8 ? r : I + r - 8;
+    const FewLane<F> ln(H);
+    const size_t wn = (size_t)(shared ? 1 : p.E) * 2 * I * ln.pitch, sn = (size_t)(shared ? 1 : p.E) * 2 * I * ln.spitch;
+    // (a unit's scale rows start at a multiple of 4 bytes)
+    const uint32_t lo = (ln.r & 7) * ln.spitch;
+    uint8_t *ring = sm.area + wave * S * SLOT;
+    const uint8_t *xs = sm.area + kFewWaves * S * SLOT;
 
-    // the unit being loaded: this lane's weight and scale rows, next chunk
-    int lu = u0, lch = 0, le = u0 / per, lc = u0 - le * per;
-    const int last = max(b1 - 1, 0);
-    const uint8_t *wrow, *srow;
+    // the step to request next: of unit lu, and where that unit's rows are
+    int lu = u0 + wave / KW, ls = s0, lslot = 0;
+    FewRows<F> rows;
     auto point = [&]() {
-        const size_t row = (size_t)(shared ? 0 : uniform(sm.expert[le])) * 2 * I + 8 * lc + my_row;
-        wrow = w + row * pitch;
-        srow = s + row * spitch;
+        const int ue = lu / per;
+        const size_t row = (size_t)(shared ? 0 : uniform(sm.expert[ue])) * 2 * I + 8 * (lu - ue * per);
+        rows.top = w + row * ln.pitch;
+        rows.low = rows.top + (size_t)I * ln.pitch;
+        rows.stop = s + row * ln.spitch;
+        rows.slow = rows.stop + (size_t)I * ln.spitch;
     };
-    u32x4 c[N][CB];
-    uint32_t sc[N][CB];
-    auto load = [&](int i) {
-#pragma unroll
-        for (int j = 0; j < CB; ++j) {
-            const int b = min(b0 + lch * CB + j, last);
-            c[i][j] = __builtin_nontemporal_load(
-                reinterpret_cast<const u32x4 *>(MOE_CHECKED(wrow + few_piece<F>(b, g, H), 16, w, rows * pitch)));
-            if constexpr (F != kFewBf16) sc[i][j] = few_scale<F>(srow, b, g, H, s, rows * spitch);
+    auto request = [&]() {
+        ln.issue(rows, ls, ring + lslot * SLOT, w, wn, s, sn);
+        lslot = lslot + 1 == S ? 0 : lslot + 1;
+        if (++ls == s1) {
+            ls = s0;
+            lu += UG;
+            if (lu < u1) point();
         }
-        if (lch + 1 < nch) {
-            ++lch;
-        } else if (lu + 1 < u1) {
-            lch = 0;
-            ++lu;
-            if (++lc == per) {
-                lc = 0;
-                ++le;
+    };
+    if (s0 == s1) lu = u1;   // more waves than steps
+    if (lu < u1) {
+        point();
+        for (int i = 0; i < S && lu < u1; ++i) request();
+    }
+    int slot = 0;
+    for (int v0 = u0; v0 < u1; v0 += UG) {
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+        if (uniform(v0 + wave / KW < u1)) {
+            for (int st = s0; st < s1; ++st) {
+                const uint8_t *q = ring + slot * SLOT;
+                // the ring is full but for this step's successors: S - 1 steps may be in flight
+                if (uniform(lu < u1)) few_wait<(S - 1) * OPS>();
+                else few_wait<0>();
+                if constexpr (F == kFewBf16) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        acc = mfma16x16x32(ln.load(q, i), few_x_frag<F, XL>(p, xs, st * FRAGS + i, r, g), acc);
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const u32x4 c = ln.load(q, h);
+                        const uint32_t sc = ln.scale(q, st, h, lo);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            acc = mfma16x16x32(few_operand<F>(c, sc, i),
+                                               few_x_frag<F, XL>(p, xs, st * FRAGS + 4 * h + i, r, g), acc);
+                    }
+                }
+                few_lds_done();
+                if (uniform(lu < u1)) request();
+                slot = slot + 1 == S ? 0 : slot + 1;
             }
-            point();
         }
-    };
-    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-    int cu = u0, cch = 0, held = 0;   // the unit being summed; units whose sums are in LDS
-    auto finish = [&]() {
-        sm.red[held][wave][lane] = acc;
-        acc = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (++held < kFewBatch && cu + 1 < u1) return;
+        sm.red[wave][lane] = acc;
         __syncthreads();
-        // wave v finishes held unit v: lane 4 t + i has token t and columns 2i, 2i + 1.  Lane 16 (m / 4) + t,
+        // wave v finishes unit v0 + v: lane 4 t + i has token t and columns 2i, 2i + 1.  Lane 16 (m / 4) + t,
         // element m % 4 of each wave's sums is weight row m, token t: gate rows 0..7, up rows 8..15
-        if (uniform(wave < held)) {
-            const int i = 2 * (lane & 3), t = lane >> 2, u = cu + 1 - held + wave, ue = u / per;
+        const int u = v0 + wave;
+        if (uniform(wave < UG && u < u1)) {
+            const int i = 2 * (lane & 3), t = lane >> 2, ue = u / per;
             float gate[2] = {0.f, 0.f}, up[2] = {0.f, 0.f};
-#pragma unroll
-            for (int v = 0; v < kFewWaves; ++v) {
-                const float *a = reinterpret_cast<const float *>(&sm.red[wave][v][16 * (i >> 2) + t]) + (i & 3);
+            for (int v = 0; v < KW; ++v) {
+                const float *a = reinterpret_cast<const float *>(&sm.red[wave * KW + v][16 * (i >> 2) + t]) + (i & 3);
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     gate[q] += a[q];
@@ -343,198 +382,198 @@ __device__ __forceinline__ void few_gateup(const FewArgs &p, FewSmem &sm, bool s
                                                                       (size_t)p.T * (shared ? 1 : p.k) * I * 2)), hv);
             }
         }
-        held = 0;
         __syncthreads();
-    };
-    point();
-#pragma unroll
-    for (int i = 0; i < N; ++i) load(i);
-    auto turn = [&](auto more) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-#pragma unroll
-            for (int j = 0; j < CB; ++j) {
-                const int b = b0 + cch * CB + j;
-                if (uniform(b < b1))
-#pragma unroll
-                    for (int q = 0; q < STEPS; ++q)
-                        acc = mfma16x16x32(few_operand<F>(c[i][j], F == kFewBf16 ? 0u : sc[i][j], q),
-                                           few_x_frag<F, XL>(p, sm, b * STEPS + q, r, g), acc);
-            }
-            if constexpr (decltype(more)::value) load(i);
-            if (++cch == nch) {
-                if (cu < u1) finish();
-                cch = 0;
-                ++cu;
-            }
-        }
-    };
-    for (int left = ((u1 - u0) * nch - 1) / N; left > 0; --left) turn(std::true_type{});
-    turn(std::false_type{});
+    }
 }
 
 // ---------------------------------------------------------------- down
-// Sixteen output columns per item: the waves take the touched experts in turn
-// (the dense MLP in pieces of about an expert's size), and their sums are
-// added in wave order.  The ring's first weights are requested before h
-// exists; h (from L2) has a ring of its own.  A lane whose token is not routed
-// to the expert multiplies another token's row, whose sums it leaves out.
-template <int F>
+// Sixteen output columns per item, summed over sub-units: the touched experts
+// (or K pieces of them, where sixteen of their rows do not fit the LDS), then
+// the dense MLP in pieces of the same size.  The waves take sub-units in turn
+// and their sums are added in wave order.  h is staged in LDS for as many
+// sub-units as fit (a pass); the ring's first weights of a pass are requested
+// before its h is staged, those of the first one before h exists.
+template <int F, int S>
+struct FewPieces {
+    // LDS for rows of h, and the largest piece of which sixteen fit
+    static constexpr int H_BYTES = kFewArea - kFewWaves * S * FewStep<F>::SLOT;
+    static constexpr int MAX = (H_BYTES / kFewTokens - 16) / (FewStep<F>::K * 2);
+    static_assert(MAX >= 1, "one step of sixteen rows fits");
+    int PW, pitch, ne, ns, U, T, A, n;   // steps of a piece, bytes of a row of it, pieces of an expert, of the MLP
+    __device__ __forceinline__ FewPieces(const FewArgs &p, int n_experts) {
+        const int st = few_steps(F, p.I), want = (st + MAX - 1) / MAX;
+        PW = (st + want - 1) / want;
+        pitch = PW * FewStep<F>::K * 2 + 16;
+        ne = (st + PW - 1) / PW;
+        ns = p.I_sh ? (few_steps(F, p.I_sh) + PW - 1) / PW : 0;
+        U = n_experts;
+        T = p.T;
+        A = p.T * p.k;
+        n = U * ne + ns;
+    }
+    // rows of h of the sub-units before v
+    __device__ __forceinline__ int rows_before(const FewSmem &sm, int v) const {
+        if (v >= U * ne) return A * ne + (v - U * ne) * T;
+        const int e = v / ne, q = v - e * ne, f = sm.first[e];
+        return f * ne + q * (sm.first[e + 1] - f);
+    }
+};
+
+template <int F, int S>
 __device__ __forceinline__ void few_down_items(const FewArgs &p, FewSmem &sm, int item) {
-    constexpr int STEPS = FewBlock<F>::STEPS, CB = FewRing<F>::CB, N = FewRing<F>::DN, M = FewRing<F>::DH;
+    constexpr int SLOT = FewStep<F>::SLOT, OPS = FewStep<F>::OPS, FRAGS = FewStep<F>::FRAGS, KS = FewStep<F>::K;
+    using P = FewPieces<F, S>;
     const int lane = threadIdx.x & 63, wave = wave_index(), r = lane & 15, g = lane >> 4;
-    const int U = uniform(sm.n_experts), pb = few_blocks(F, p.I);
-    const int n = U + (p.I_sh ? (few_blocks(F, p.I_sh) + pb - 1) / pb : 0);   // sub-units: experts, pieces of the dense MLP
-    // blocks [b0, b1) of sub-unit v, whose rows are `width` values
-    auto span = [&](int v, int &b0, int &b1, int &width) {
-        width = v < U ? p.I : p.I_sh;
-        b0 = v < U ? 0 : (v - U) * pb;
-        b1 = min(few_blocks(F, width), b0 + pb);
-    };
-    // slot + 1 of this lane's token in sub-unit v (0: not routed there)
-    auto route = [&](int v) -> int { return r < p.T ? (v >= U ? 1 : (int)sm.slot[v][r]) : 0; };
+    const P pc(p, uniform(sm.n_experts));
+    const int UE = pc.U * pc.ne;
+    uint8_t *ring = sm.area + wave * S * SLOT;
+    uint8_t *hs = sm.area + kFewWaves * S * SLOT;
 
-    u32x4 c[N][CB], h[M][CB][STEPS];
-    uint32_t sc[N][CB];
-    // the sub-unit whose weights are being loaded: its next block, its end
-    int lv = 0, lb = 0, lb1 = 0, lI = 0;
-    const uint8_t *wrow = nullptr, *srow = nullptr;
-    [[maybe_unused]] const uint8_t *wbase = nullptr, *sbase = nullptr;
-    [[maybe_unused]] size_t wbytes = 0, sbytes = 0;
+    int va = 0, vb = 0;              // the pass: sub-units va .. vb - 1
+    int lv = 0, ls = 0, ls1 = 0, lslot = 0;   // next step to request: of sub-unit lv
+    FewRows<F> rows;
+    auto steps = [&](int v, int &a, int &b) {   // steps [a, b) of its row that sub-unit v covers
+        const int q = v < UE ? v % pc.ne : v - UE;
+        a = q * pc.PW;
+        b = min(few_steps(F, v < UE ? p.I : p.I_sh), a + pc.PW);
+    };
     auto point = [&]() {
-        const bool shared = lv >= U;
-        span(lv, lb, lb1, lI);
-        const size_t row = (size_t)(shared ? 0 : uniform(sm.expert[lv])) * p.H + 16 * item + r;
-        const size_t pitch = F == kFewBf16 ? (size_t)lI * 2 : (size_t)lI / 2, spitch = F == kFewMx ? lI / 32 : lI / 16;
-        wbase = shared ? p.swd : p.wd;
-        sbase = shared ? p.sds : p.ds;
-        wbytes = (size_t)(shared ? 1 : p.E) * p.H * pitch;
-        sbytes = (size_t)(shared ? 1 : p.E) * p.H * spitch;
-        wrow = wbase + row * pitch;
-        srow = sbase + row * spitch;
+        const bool mlp = lv >= UE;
+        const size_t row = (size_t)(mlp ? 0 : uniform(sm.expert[lv / pc.ne])) * p.H + 16 * item;
+        const FewLane<F> ln(mlp ? p.I_sh : p.I);
+        rows.top = (mlp ? p.swd : p.wd) + row * ln.pitch;
+        rows.low = rows.top + (size_t)8 * ln.pitch;
+        rows.stop = (mlp ? p.sds : p.ds) + row * ln.spitch;
+        rows.slow = rows.stop + (size_t)8 * ln.spitch;
+        steps(lv, ls, ls1);
     };
-    auto load = [&](int i) {
-#pragma unroll
-        for (int j = 0; j < CB; ++j) {
-            const int b = min(lb + j, lb1 - 1);
-            c[i][j] = __builtin_nontemporal_load(
-                reinterpret_cast<const u32x4 *>(MOE_CHECKED(wrow + few_piece<F>(b, g, lI), 16, wbase, wbytes)));
-            if constexpr (F != kFewBf16) sc[i][j] = few_scale<F>(srow, b, g, lI, sbase, sbytes);
-        }
-        if (lb + CB < lb1) {
-            lb += CB;
-        } else if (lv + kFewWaves < n) {
+    auto request = [&]() {
+        uint8_t *q = ring + lslot * SLOT;
+        const bool mlp = lv >= UE;
+        const FewLane<F> ln(mlp ? p.I_sh : p.I);
+        const size_t nr = (size_t)(mlp ? 1 : p.E) * p.H;
+        ln.issue(rows, ls, q, mlp ? p.swd : p.wd, nr * ln.pitch, mlp ? p.sds : p.ds, nr * ln.spitch);
+        lslot = lslot + 1 == S ? 0 : lslot + 1;
+        if (++ls == ls1) {
             lv += kFewWaves;
+            if (lv < vb) point();
+        }
+    };
+    // the next pass, as many sub-units as fit, and its first requests
+    auto next_pass = [&](int from) {
+        va = from;
+        const int base = pc.rows_before(sm, va), most = P::H_BYTES / pc.pitch;
+        vb = va;
+        for (;;) {   // 64 candidates at a time; the rows only grow
+            const int v = vb + 1 + lane;
+            const int fit = __popcll(__ballot(v <= pc.n && pc.rows_before(sm, min(v, pc.n)) - base <= most));
+            vb += fit;
+            if (fit < 64) break;
+        }
+        vb = uniform(vb);
+        lv = va + wave;
+        lslot = 0;
+        if (lv < vb) {
             point();
+            for (int i = 0; i < S && lv < vb; ++i) request();
         }
     };
-    auto start = [&]() {
-        lv = wave;
-        if (lv >= n) return;
-        point();
-#pragma unroll
-        for (int i = 0; i < N; ++i) load(i);
-    };
-    // the sub-unit whose h is being loaded, and this lane's h row (where its
-    // token is not routed there, the row of one that is)
-    int hv = 0, hb = 0, hb1 = 0, hI = 0;
-    const uint16_t *hrow = nullptr;
-    [[maybe_unused]] const uint16_t *hbase = nullptr;
-    [[maybe_unused]] size_t hbytes = 0;
-    auto point_h = [&]() {
-        const bool shared = hv >= U;
-        span(hv, hb, hb1, hI);
-        const int j = route(hv), mine = shared ? r : r * p.k + j - 1;
-        const int other = __builtin_amdgcn_readlane(mine, (int)__builtin_ctzll(__ballot(j != 0) | (1ull << 63)));
-        hbase = shared ? p.h_sh : p.h;
-        hbytes = (size_t)p.T * (shared ? 1 : p.k) * hI * 2;
-        hrow = hbase + (size_t)(j ? mine : other) * hI;
-    };
-    auto load_h = [&](int i) {
-#pragma unroll
-        for (int j = 0; j < CB; ++j) {
-            const int b = min(hb + j, hb1 - 1);
-#pragma unroll
-            for (int q = 0; q < STEPS; ++q) {
-                const int k = few_frag_k<F>(b * STEPS + q, g);
-                h[i][j][q] = *reinterpret_cast<const u32x4 *>(MOE_CHECKED(hrow + (k < hI ? k : 0), 16, hbase, hbytes));
-            }
-        }
-        if (hb + CB < hb1) {
-            hb += CB;
-        } else if (hv + kFewWaves < n) {
-            hv += kFewWaves;
-            point_h();
-        }
-    };
-
     for (bool have_h = false;;) {
-        // wave 0 polls for h, and loads return in order: its weights only after that
-        if (wave != 0) start();
-        if (threadIdx.x == 0) {
-            if (!have_h) wait_count(p.ctr + kCtrGateUp, p.n_gu);
-            sm.down = (int)ctr_add(p.ctr + kCtrDownTicket);
-        }
-        have_h = true;
-        __syncthreads();
-        if (wave == 0) start();
-        const int next = uniform(sm.down);
         f32x4 out = {0.f, 0.f, 0.f, 0.f};
-        if (wave < n) {
-            hv = wave;
-            point_h();
-#pragma unroll
-            for (int i = 0; i < M; ++i) load_h(i);
-            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-            int cv = wave, cb, cb1, cI;
-            span(cv, cb, cb1, cI);
-            auto turn = [&](auto more) {
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-#pragma unroll
-                    for (int j = 0; j < CB; ++j) {
-                        if (uniform(cb + j < cb1)) {
-                            u32x4 cw = c[i][j];
-                            if constexpr (F != kFewBf16) {
-                                // codes past the row (the last block of an odd number of half blocks) count as zero
-                                if (128 * (cb + j) + 32 * g >= cI) cw = u32x4{0u, 0u, 0u, 0u};
-                            }
-#pragma unroll
-                            for (int q = 0; q < STEPS; ++q)
-                                acc = mfma16x16x32(few_operand<F>(cw, F == kFewBf16 ? 0u : sc[i][j], q), h[i % M][j][q], acc);
-                        }
-                    }
-                    if constexpr (decltype(more)::value) load(i);
-                    if (decltype(more)::value || i + M < N) load_h(i % M);
-                    cb += CB;
-                    if (cb >= cb1 && cv < n) {
-                        const int j = route(cv);
-                        float f = cv >= U ? 1.f : sm.w[j ? r * p.k + j - 1 : 0];
-                        if constexpr (F == kFewNv) f *= cv >= U ? p.sdg[0] : p.dg[uniform(sm.expert[cv])];
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) out[q] = j ? fmaf(f, acc[q], out[q]) : out[q];
-                        acc = f32x4{0.f, 0.f, 0.f, 0.f};
-                        cv += kFewWaves;
-                        if (cv < n) span(cv, cb, cb1, cI);
+        int next = 0;
+        for (int from = 0; from < pc.n; from = vb) {
+            // wave 0 polls for h, and loads return in order: its first weights only after that
+            if (wave != 0 || have_h) next_pass(from);
+            if (from == 0) {
+                if (threadIdx.x == 0) {
+                    if (!have_h) wait_count(p.ctr + kCtrGateUp, p.n_gu);
+                    sm.down = (int)ctr_add(p.ctr + kCtrDownTicket);
+                }
+                __syncthreads();
+                next = uniform(sm.down);
+                if (wave == 0 && !have_h) next_pass(from);
+                have_h = true;
+            }
+            // stage the pass's rows of h: sub-unit by sub-unit, its rows in token order
+            const int base = pc.rows_before(sm, va);
+            for (int v = va + wave; v < vb; v += kFewWaves) {
+                const bool mlp = v >= UE;
+                const int e = v / pc.ne, f = mlp ? 0 : uniform(sm.first[e]);
+                const int nr = mlp ? p.T : uniform(sm.first[e + 1]) - f, I = mlp ? p.I_sh : p.I;
+                int a, b;
+                steps(v, a, b);
+                const int valid = (min(I, b * KS) - a * KS) / 8, all = (b - a) * (KS / 8);   // 16-byte pieces of a row
+                uint8_t *dst = hs + (size_t)(uniform(pc.rows_before(sm, v)) - base) * pc.pitch;
+                for (int i = 0; i < nr; ++i, dst += pc.pitch) {
+                    const uint16_t *hb = mlp ? p.h_sh : p.h;
+                    const uint16_t *src = hb + (size_t)(mlp ? i : uniform(sm.sorted[f + i])) * I + a * KS;
+                    for (int c = 0; c < all; c += 64) {
+                        if (c + lane < valid)
+                            dma16<false>(MOE_CHECKED(src + 8 * (c + lane), 16, hb, (size_t)p.T * (mlp ? 1 : p.k) * I * 2),
+                                         dst + 16 * c);
+                        else if (c + lane < all)   // past the row: the codes there count nothing
+                            *reinterpret_cast<u32x4 *>(dst + 16 * (c + lane)) = u32x4{0u, 0u, 0u, 0u};
                     }
                 }
-            };
-            int chunks = 0;
-            for (int v = wave; v < n; v += kFewWaves) {
-                int v0, v1, vI;
-                span(v, v0, v1, vI);
-                chunks += (v1 - v0 + CB - 1) / CB;
             }
-            for (int left = (chunks - 1) / N; left > 0; --left) turn(std::true_type{});
-            turn(std::false_type{});
+            few_wait<0>();
+            __syncthreads();
+            int slot = 0;
+            for (int v = va + wave; v < vb; v += kFewWaves) {
+                const bool mlp = v >= UE;
+                const int e = v / pc.ne;
+                int a, b;
+                steps(v, a, b);
+                // this lane's row: its token's, or, where that is not routed here, the first one (left out below)
+                int j = r < p.T, rank = r;
+                if (!mlp) {
+                    j = sm.slot[e][r];
+                    rank = few_count(*reinterpret_cast<const u32x4 *>(sm.slot[e]), r);
+                }
+                const uint8_t *hr = hs + (size_t)(pc.rows_before(sm, v) - base + (j ? rank : 0)) * pc.pitch;
+                const FewLane<F> ln(mlp ? p.I_sh : p.I);
+                const uint32_t lo = (ln.r & 7) * ln.spitch;
+                f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+                for (int st = a; st < b; ++st) {
+                    const uint8_t *q = ring + slot * SLOT;
+                    if (uniform(lv < vb)) few_wait<(S - 1) * OPS>();
+                    else few_wait<0>();
+                    const uint8_t *hk = hr + 2 * KS * (st - a);
+                    if constexpr (F == kFewBf16) {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            acc = mfma16x16x32(ln.load(q, i), *reinterpret_cast<const u32x4 *>(hk + 2 * few_frag_k<F>(i, g)),
+                                               acc);
+                    } else {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const u32x4 c = ln.load(q, h);
+                            const uint32_t sc = ln.scale(q, st, h, lo);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                acc = mfma16x16x32(
+                                    few_operand<F>(c, sc, i),
+                                    *reinterpret_cast<const u32x4 *>(hk + 2 * few_frag_k<F>(4 * h + i, g)), acc);
+                        }
+                    }
+                    few_lds_done();
+                    if (uniform(lv < vb)) request();
+                    slot = slot + 1 == S ? 0 : slot + 1;
+                }
+                float f = mlp ? 1.f : sm.w[j ? r * p.k + j - 1 : 0];
+                if constexpr (F == kFewNv) f *= mlp ? p.sdg[0] : p.dg[uniform(sm.expert[e])];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) out[q] = j ? fmaf(f, acc[q], out[q]) : out[q];
+            }
+            if (vb < pc.n) __syncthreads();   // the rows of h are free
         }
-        sm.red[0][wave][lane] = out;
+        sm.red[wave][lane] = out;
         __syncthreads();
         if (threadIdx.x < 256) {
             const int m = threadIdx.x & 15, t = threadIdx.x >> 4;
             float sum = 0.f;
 #pragma unroll
-            for (int v = 0; v < kFewWaves; ++v) sum += sm.red[0][v][16 * (m >> 2) + t][m & 3];
+            for (int v = 0; v < kFewWaves; ++v) sum += sm.red[v][16 * (m >> 2) + t][m & 3];
             if (t < p.T)
                 *MOE_CHECKED(p.out + (size_t)t * p.H + 16 * item + m, 2, p.out, (size_t)p.T * p.H * 2) =
                     (uint16_t)f32_to_bf16_rne(sum);
@@ -543,15 +582,13 @@ __device__ __forceinline__ void few_down_items(const FewArgs &p, FewSmem &sm, in
         item = next;
         if ((uint32_t)item >= (uint32_t)p.n_down) return;
     }
+    static_assert(FRAGS * 32 == KS);
 }
 
-// XL: the token rows fit the LDS.
-template <int F, bool XL>
+// S: steps in each wave's ring.  XL: the token rows fit the LDS next to the rings.
+template <int F, int S, bool XL>
 __global__ __launch_bounds__(kFewThreads) void few_layer_kernel(FewArgs p) {
     __shared__ FewSmem sm;
-    const int wave = wave_index();
-    // tickets: a router item (then more, while there are any), then a gate/up
-    // share and a down item together
     if (threadIdx.x == 0) sm.ticket = (int)ctr_add(p.ctr + kCtrRouterTicket);
     __syncthreads();
     for (int t = uniform(sm.ticket); (uint32_t)t < (uint32_t)p.n_router;) {
@@ -574,34 +611,48 @@ __global__ __launch_bounds__(kFewThreads) void few_layer_kernel(FewArgs p) {
         sm.ticket = (int)a;
         sm.down = (int)b;
     }
-    if constexpr (XL) few_stage_x<F>(p, sm);
+    if constexpr (XL) few_stage_x<F>(p, sm.area + kFewWaves * S * FewStep<F>::SLOT);
     __syncthreads();
     int t = uniform(sm.ticket);
     const int d = uniform(sm.down);
-    if (p.I_sh && (uint32_t)t < (uint32_t)p.n_gu) {   // needs no routing
-        const int units = p.I_sh / 8;
-        few_gateup<F, XL>(p, sm, true, share_start(t, units, p.n_gu), share_start(t + 1, units, p.n_gu));
-    }
-    few_select(p, sm, t == 0);
-    for (bool first = true; (uint32_t)t < (uint32_t)p.n_gu; first = false) {
+    bool selected = false;
+    for (;;) {
+        const bool share = (uint32_t)t < (uint32_t)p.n_gu;
+        if (share && p.I_sh) {   // needs no routing
+            const int units = p.I_sh / 8;
+            few_gateup<F, S, XL>(p, sm, true, share_start(t, units, p.n_gu), share_start(t + 1, units, p.n_gu));
+        }
+        if (!selected) few_select(p, sm, t == 0);
+        selected = true;
+        if (!share) break;
         // the next ticket, early: none is left unless a workgroup has not started yet
         if (threadIdx.x == 0) sm.ticket = (int)ctr_add(p.ctr + kCtrGateUpTicket);
-        if (!first && p.I_sh) {
-            const int units = p.I_sh / 8;
-            few_gateup<F, XL>(p, sm, true, share_start(t, units, p.n_gu), share_start(t + 1, units, p.n_gu));
-        }
         const int units = uniform(sm.n_experts) * (p.I / 8);
-        few_gateup<F, XL>(p, sm, false, share_start(t, units, p.n_gu), share_start(t + 1, units, p.n_gu));
+        few_gateup<F, S, XL>(p, sm, false, share_start(t, units, p.n_gu), share_start(t + 1, units, p.n_gu));
         publish(p.ctr + kCtrGateUp);
         t = uniform(sm.ticket);
         __syncthreads();
+        if ((uint32_t)t >= (uint32_t)p.n_gu) break;
     }
-    if ((uint32_t)d < (uint32_t)p.n_down) few_down_items<F>(p, sm, d);
+    if ((uint32_t)d < (uint32_t)p.n_down) few_down_items<F, S>(p, sm, d);
     // the last workgroup to leave clears the counters for the next call
     if (threadIdx.x == 0 && ctr_add(p.ctr + kCtrExit) == gridDim.x - 1) {
         const int all[6] = {kCtrRouterTicket, kCtrGateUpTicket, kCtrDownTicket, kCtrRouter, kCtrGateUp, kCtrExit};
         for (int c : all) __hip_atomic_store(p.ctr + c, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
+}
+
+// The deepest of three rings that leaves the token rows room; rows that are
+// too long for any are read from global memory.
+template <int F, int S0, int S1, int S2>
+void launch_format(const FewArgs &p, int blocks, hipStream_t st) {
+    const size_t x = (size_t)few_steps(F, p.H) * FewStep<F>::K * 2 * p.T;
+    auto fits = [&](int s) { return x <= (size_t)(kFewArea - kFewWaves * s * FewStep<F>::SLOT); };
+    const dim3 grid(blocks), block(kFewThreads);
+    if (fits(S0)) few_layer_kernel<F, S0, true><<<grid, block, 0, st>>>(p);
+    else if (fits(S1)) few_layer_kernel<F, S1, true><<<grid, block, 0, st>>>(p);
+    else if (fits(S2)) few_layer_kernel<F, S2, true><<<grid, block, 0, st>>>(p);
+    else few_layer_kernel<F, S1, false><<<grid, block, 0, st>>>(p);
 }
 
 }  // namespace
@@ -643,20 +694,10 @@ hipError_t launch_few_layer(const FewLayer &l, hipStream_t st) {
     p.n_gu = (int)std::min<long long>(kBlocks, std::max<long long>(units, l.I_sh / 8));
     p.n_down = l.H / 16;
     const int blocks = std::min(kBlocks, std::max(p.n_router, std::max(p.n_gu, p.n_down)));
-    const dim3 grid(blocks), block(kFewThreads);
-    const bool fits = ((size_t)l.H + 127) / 128 * 256 * l.T <= kFewXBytes;
     switch (l.fmt) {
-        case WeightFormat::kBF16:
-            if (fits) few_layer_kernel<kFewBf16, true><<<grid, block, 0, st>>>(p);
-            else few_layer_kernel<kFewBf16, false><<<grid, block, 0, st>>>(p);
-            break;
-        case WeightFormat::kMXFP4:
-            if (fits) few_layer_kernel<kFewMx, true><<<grid, block, 0, st>>>(p);
-            else few_layer_kernel<kFewMx, false><<<grid, block, 0, st>>>(p);
-            break;
-        default:
-            if (fits) few_layer_kernel<kFewNv, true><<<grid, block, 0, st>>>(p);
-            else few_layer_kernel<kFewNv, false><<<grid, block, 0, st>>>(p);
+        case WeightFormat::kBF16: launch_format<kFewBf16, 7, 5, 3>(p, blocks, st); break;
+        case WeightFormat::kMXFP4: launch_format<kFewMx, 5, 4, 2>(p, blocks, st); break;
+        default: launch_format<kFewNv, 5, 4, 2>(p, blocks, st);
     }
     return hipGetLastError();
 }

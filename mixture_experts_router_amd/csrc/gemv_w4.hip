@@ -4,11 +4,11 @@
 //
 // A weight is read once and multiplied with every token (few_stream.h), so
 // the weight bytes bound the product.  A workgroup keeps the token rows of its
-// K range in LDS in MFMA order and runs through a range of 16-row units, its
-// waves splitting K; sums are fp32 and rounded once.  Where the token rows of
-// the whole K exceed the LDS, or the units are too few to fill the GPU, several
-// workgroups share a range along K: each stores its fp32 sums, and the last to
-// finish adds them in K order, whichever it is.
+// K range in LDS in MFMA order and runs through a range of 16-row units; a
+// unit's K is split over as many of its waves as the range leaves free.  Sums
+// are fp32 and rounded once.  Where the token rows of the whole K exceed the
+// LDS, several workgroups share a range along K: each stores its fp32 sums,
+// and the last to finish adds them in K order, whichever it is.
 //
 // INT4: W = scale (code - zero) with one scale and zero per group of 32, 64 or
 // 128 K values.  The matrix cores multiply the exact values 16 + code, one
@@ -24,8 +24,8 @@ namespace moe {
 namespace {
 
 constexpr int kGemvWaves = 8, kGemvThreads = 64 * kGemvWaves;
-constexpr int kGemvXBytes = 128 * 1024;
-constexpr int kGemvBlocks = 256;    // a workgroup per CU
+constexpr int kGemvArea = 150 * 1024;   // LDS for the rings, the token rows and (INT4) their sums
+constexpr int kGemvBlocks = 256;        // a workgroup per CU
 
 struct GemvArgs {
     const uint16_t *x;
@@ -43,12 +43,21 @@ struct GemvArgs {
 };
 
 struct GemvSmem {
-    uint8_t x[kGemvXBytes];
-    float xsum[kGemvXBytes / 2 / 32];          // INT4: token sums [group][token]
-    f32x4 red[2][kGemvWaves][64];
+    alignas(1024) uint8_t area[kGemvArea];
+    f32x4 red[kGemvWaves][64];
     int last;
 };
 static_assert(sizeof(GemvSmem) <= 160 * 1024, "LDS of one workgroup");
+
+// A ring slot of the formats here: the step's codes, then its scales (and
+// zeros): aligned words that hold the wanted bytes, 64 to a load.  INT4 loads
+// the words of (row l % 16, group l / 16 + 4 i).
+template <int F, int GROUP, bool ZEROS>
+struct GemvSlot {
+    static constexpr int NS = F == kFewI4 ? (GROUP == 32 ? 2 : 1) : 0;
+    static constexpr int SLOT = FewStep<F>::SLOT + 256 * NS * (ZEROS ? 2 : 1);
+    static constexpr int OPS = FewStep<F>::OPS + NS * (ZEROS ? 2 : 1);
+};
 
 // Weight row of the MFMA's row m in unit u, clamped to a row that exists (the
 // results of the others are not stored).
@@ -82,102 +91,173 @@ __device__ __forceinline__ void gemv_store(const GemvArgs &p, int u, int m, int 
     else *MOE_CHECKED(static_cast<uint16_t *>(p.y) + at, 2, p.y, vals * 2) = (uint16_t)f32_to_bf16_rne(sum);
 }
 
-template <int F, int GROUP>
+// S: steps in each wave's ring.
+template <int F, int GROUP, bool ZEROS, int S>
 __global__ __launch_bounds__(kGemvThreads) void gemv_w4_kernel(GemvArgs p) {
     __shared__ GemvSmem sm;
-    constexpr int STEPS = FewBlock<F>::STEPS;
+    using G = GemvSlot<F, GROUP, ZEROS>;
+    constexpr int SLOT = G::SLOT, OPS = G::OPS, FRAGS = FewStep<F>::FRAGS;
     const int lane = threadIdx.x & 63, wave = wave_index(), r = lane & 15, g = lane >> 4;
     const int range = blockIdx.x / p.slices, slice = blockIdx.x % p.slices;
-    const int nb = few_blocks(F, p.K);
-    const int s0 = (int)((long long)slice * nb / p.slices), s1 = (int)((long long)(slice + 1) * nb / p.slices);
+    const int nst = few_steps(F, p.K);
+    const int c0 = (int)((long long)slice * nst / p.slices), c1 = (int)((long long)(slice + 1) * nst / p.slices);
     const int u0 = (int)((long long)range * p.units / p.ranges), u1 = (int)((long long)(range + 1) * p.units / p.ranges);
     const int T = p.T, K = p.K, tr = min(r, T - 1);
+    const int KW = few_kwaves(u1 - u0, c1 - c0), UG = kGemvWaves / KW, kw = wave % KW;
+    const int s0 = c0 + kw * (c1 - c0) / KW, s1 = c0 + (kw + 1) * (c1 - c0) / KW;
+    const FewLane<F> ln(K);
+    uint8_t *ring = sm.area + wave * S * SLOT, *xs = sm.area + kGemvWaves * S * SLOT;
+    const int nx = (c1 - c0) * FRAGS * 4 * T;   // 16-byte pieces of the token rows
+    [[maybe_unused]] float *xsum = reinterpret_cast<float *>(xs + (size_t)nx * 16);
     [[maybe_unused]] const size_t xbytes = (size_t)((T - 1) * p.ldx + K) * 2;
+    const size_t wn = (size_t)p.N * ln.pitch;
+    [[maybe_unused]] const int pg = GROUP ? K / (GROUP ? GROUP : 1) : 0;   // groups of a row
+    const size_t sn = (size_t)p.N * (F == kFewI4 ? 2 * pg : (int)ln.spitch);
+
+    // the step to request next: of unit lu
+    int lu = u0 + wave / KW, ls = s0, lslot = 0;
+    FewRows<F> rows;
+    [[maybe_unused]] size_t lgroup = 0;         // INT4: first group of this lane's row (MFMA row lane % 16)
+    auto point = [&]() {
+        const int top = p.geglu ? 8 * lu : 16 * lu, low = p.geglu ? p.outs + top : min(top + 8, p.N - 1);
+        rows.ntop = min(7, (p.geglu ? p.outs : p.N) - 1 - top);
+        rows.nlow = p.geglu ? rows.ntop : min(7, p.N - 1 - low);
+        rows.top = p.w + (size_t)top * ln.pitch;
+        rows.low = p.w + (size_t)low * ln.pitch;
+        rows.stop = p.scales + (size_t)top * ln.spitch;
+        rows.slow = p.scales + (size_t)low * ln.spitch;
+        if constexpr (F == kFewI4) lgroup = (size_t)gemv_row(p, lu, r) * pg;
+    };
+    auto request = [&]() {
+        uint8_t *q = ring + lslot * SLOT;
+        ln.issue(rows, ls, q, p.w, wn, p.scales, sn);
+        if constexpr (F == kFewI4) {
+#pragma unroll
+            for (int i = 0; i < G::NS; ++i) {
+                const int j = ls * (256 / GROUP) + g + 4 * i;
+                const size_t at = lgroup + (j < pg ? j : 0);
+                dma4(MOE_CHECKED(p.scales + 2 * (at & ~(size_t)1), 4, p.scales, (sn + 3) & ~(size_t)3), q + 2048 + 256 * i);
+                if constexpr (ZEROS)
+                    dma4(MOE_CHECKED(p.zeros + (at & ~(size_t)3), 4, p.zeros, ((size_t)p.N * pg + 3) & ~(size_t)3),
+                         q + 2048 + 256 * (G::NS + i));
+            }
+        }
+        lslot = lslot + 1 == S ? 0 : lslot + 1;
+        if (++ls == s1) {
+            ls = s0;
+            lu += UG;
+            if (lu < u1) point();
+        }
+    };
+    if (s0 == s1) lu = u1;   // more waves than steps
+    if (lu < u1) {
+        point();
+        for (int i = 0; i < S && lu < u1; ++i) request();
+    }
 
     // token rows of this K range, zero past K
-    for (int i = threadIdx.x; i < (s1 - s0) * STEPS * 4 * T; i += kGemvThreads) {
-        const int t = i % T, fg = i / T, k = few_frag_k<F>(s0 * STEPS + (fg >> 2), fg & 3);
+    for (int i = threadIdx.x; i < nx; i += kGemvThreads) {
+        const int t = i % T, fg = i / T, k = few_frag_k<F>(c0 * FRAGS + (fg >> 2), fg & 3);
         u32x4 v = {0u, 0u, 0u, 0u};
         if (k < K) v = *reinterpret_cast<const u32x4 *>(MOE_CHECKED(p.x + t * p.ldx + k, 16, p.x, xbytes));
-        *reinterpret_cast<u32x4 *>(sm.x + (size_t)i * 16) = F == kFewI4 ? few_i4_order(v) : v;
+        *reinterpret_cast<u32x4 *>(xs + (size_t)i * 16) = F == kFewI4 ? few_i4_order(v) : v;
     }
     __syncthreads();
     if constexpr (F == kFewI4) {
-        const int per = GROUP / 8;   // 16-byte pieces of one group and token, at stride 16 T
-        for (int i = threadIdx.x; i < (s1 - s0) * (128 / GROUP) * T; i += kGemvThreads) {
+        constexpr int per = GROUP / 8;   // 16-byte pieces of one group and token, at stride 16 T
+        for (int i = threadIdx.x; i < nx / per; i += kGemvThreads) {
             const int t = i % T, grp = i / T;
             float s = 0.f;
             for (int j = 0; j < per; ++j) {
-                const u32x4 v = *reinterpret_cast<const u32x4 *>(sm.x + ((size_t)(grp * per + j) * T + t) * 16);
+                const u32x4 v = *reinterpret_cast<const u32x4 *>(xs + ((size_t)(grp * per + j) * T + t) * 16);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) s += bf16_to_f32(v[q] & 0xFFFFu) + bf16_to_f32(v[q] >> 16);
             }
-            sm.xsum[i] = s;
+            xsum[i] = s;
         }
         __syncthreads();
     }
 
-    const int b0 = s0 + wave * (s1 - s0) / kGemvWaves, b1 = s0 + (wave + 1) * (s1 - s0) / kGemvWaves;
-    const size_t pitch = (size_t)K / 2, spitch = F == kFewI4 ? K / (GROUP ? GROUP : 1) : (F == kFewMx ? K / 32 : K / 16);
-    [[maybe_unused]] const size_t wbytes = (size_t)p.N * pitch, sbytes = (size_t)p.N * spitch;
-    for (int u = u0; u < u1; ++u) {
-        const uint8_t *wrow = p.w + gemv_row(p, u, r) * pitch;
-        const uint8_t *srow = F == kFewI4 ? nullptr : p.scales + gemv_row(p, u, r) * spitch;
-        size_t grow[4];   // INT4: first group of the four weight rows whose sums this lane holds
-#pragma unroll
-        for (int q = 0; q < 4; ++q) grow[q] = gemv_row(p, u, 4 * g + q) * spitch;
+    const uint8_t *xl = xs + (g * T + tr) * 16;   // this lane's piece of a token fragment
+    int slot = 0;
+    for (int v0 = u0; v0 < u1; v0 += UG) {
         f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
-        for (int b = b0; b < b1; ++b) {
-            u32x4 c = __builtin_nontemporal_load(
-                reinterpret_cast<const u32x4 *>(MOE_CHECKED(wrow + few_piece<F>(b, g, K), 16, p.w, wbytes)));
+        const int u = v0 + wave / KW;
+        if (uniform(u < u1)) {
+            // where in its word a scale (zero) of this lane's rows lies: the low bits of its index
+            [[maybe_unused]] uint32_t lo = 0, low4[4];
             if constexpr (F == kFewI4) {
-                few_transpose(c);
-                f32x4 part = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int i = 0; i < STEPS; ++i) {
-                    const int f = b * STEPS + i, fl = f - s0 * STEPS;
-                    part = mfma16x16x32(few_i4_operand(c[i]),
-                                        *reinterpret_cast<const u32x4 *>(sm.x + ((size_t)(fl * 4 + g) * T + tr) * 16), part);
-                    if ((i + 1) * 32 % GROUP) continue;
-                    if (32 * f < K) {
-                        const float xs = sm.xsum[fl * 32 / GROUP * T + tr];
+                for (int q = 0; q < 4; ++q) low4[q] = (uint32_t)gemv_row(p, u, 4 * g + q) * (uint32_t)pg;
+            } else {
+                lo = (uint32_t)reinterpret_cast<uintptr_t>(p.scales) + (uint32_t)gemv_row(p, u, r) * ln.spitch;
+            }
+            for (int st = s0; st < s1; ++st) {
+                const uint8_t *q = ring + slot * SLOT;
+                if (uniform(lu < u1)) few_wait<(S - 1) * OPS>();
+                else few_wait<0>();
+                const uint8_t *xq = xl + (size_t)(st - c0) * FRAGS * 64 * T;
+                if constexpr (F == kFewI4) {
+                    f32x4 part = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const size_t at = grow[q] + 32 * f / GROUP;
-                            const float s = bf16_to_f32(*reinterpret_cast<const uint16_t *>(
-                                MOE_CHECKED(p.scales + 2 * at, 2, p.scales, sbytes * 2)));
-                            const float z = p.zeros ? (float)*MOE_CHECKED(p.zeros + at, 1, p.zeros, sbytes) : 8.f;
-                            acc[q] = fmaf(s, fmaf(-(16.f + z), xs, part[q]), acc[q]);
+                    for (int h = 0; h < 2; ++h) {
+                        u32x4 c = ln.load(q, h);
+                        few_transpose(c);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int f = 4 * h + i, j = f * 32 / GROUP;
+                            part = mfma16x16x32(few_i4_operand(c[i]), *reinterpret_cast<const u32x4 *>(xq + f * 64 * T), part);
+                            if ((i + 1) * 32 % GROUP) continue;
+                            const int grp = st * (256 / GROUP) + j;
+                            if (uniform(grp < pg)) {
+                                const float xv = xsum[(grp - c0 * (256 / GROUP)) * T + tr];
+                                const u32x4 sw = *reinterpret_cast<const u32x4 *>(q + 2048 + 4 * (16 * j + 4 * g));
+                                u32x4 zw = {8u, 8u, 8u, 8u};
+                                if constexpr (ZEROS)
+                                    zw = *reinterpret_cast<const u32x4 *>(q + 2048 + 256 * G::NS + 4 * (16 * j + 4 * g));
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const uint32_t at = low4[e] + grp;
+                                    const float s = __uint_as_float(at & 1 ? sw[e] & 0xFFFF0000u : sw[e] << 16);
+                                    const float z = ZEROS ? (float)((zw[e] >> (8 * (at & 3))) & 0xFFu) : 8.f;
+                                    acc[e] = fmaf(s, fmaf(-(16.f + z), xv, part[e]), acc[e]);
+                                }
+                            }
+                            part = f32x4{0.f, 0.f, 0.f, 0.f};
                         }
                     }
-                    part = f32x4{0.f, 0.f, 0.f, 0.f};
-                }
-            } else {
-                const uint32_t sc = few_scale<F>(srow, b, g, K, p.scales, sbytes);
+                } else {
 #pragma unroll
-                for (int i = 0; i < STEPS; ++i) {
-                    const int fl = (b - s0) * STEPS + i;
-                    acc = mfma16x16x32(few_operand<F>(c, sc, i),
-                                       *reinterpret_cast<const u32x4 *>(sm.x + ((size_t)(fl * 4 + g) * T + tr) * 16), acc);
+                    for (int h = 0; h < 2; ++h) {
+                        const u32x4 c = ln.load(q, h);
+                        const uint32_t sc = ln.scale(q, st, h, lo);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            acc = mfma16x16x32(few_operand<F>(c, sc, i),
+                                               *reinterpret_cast<const u32x4 *>(xq + (4 * h + i) * 64 * T), acc);
+                    }
                 }
+                few_lds_done();
+                if (uniform(lu < u1)) request();
+                slot = slot + 1 == S ? 0 : slot + 1;
             }
         }
-        f32x4(*red)[64] = sm.red[u & 1];
-        red[wave][lane] = acc;
+        sm.red[wave][lane] = acc;
         __syncthreads();
-        // lane 16 (m / 4) + t, element m % 4 of each wave's sums: weight row m, token t
-        if (threadIdx.x < 256) {
-            const int m = threadIdx.x & 15, t = threadIdx.x >> 4;
-            float sum = 0.f;
-#pragma unroll
-            for (int v = 0; v < kGemvWaves; ++v) sum += red[v][16 * (m >> 2) + t][m & 3];
-            if (p.slices == 1)
-                gemv_store<F>(p, u, m, t, sum);
-            else if (t < T)
-                *MOE_CHECKED(p.part + (((size_t)u * p.slices + slice) * T + t) * 16 + m, 4, p.part,
-                             (size_t)p.units * p.slices * T * 64) = sum;
+        // four waves finish a unit (lane 16 (m / 4) + t, element m % 4 of each wave's sums: weight row m, token t)
+        for (int i = wave; i < 4 * UG; i += kGemvWaves) {
+            const int unit = v0 + (i >> 2), m = lane & 15, t = 4 * (i & 3) + (lane >> 4);
+            if (uniform(unit < u1 && 4 * (i & 3) < T)) {
+                float sum = 0.f;
+                for (int v = 0; v < KW; ++v) sum += sm.red[(i >> 2) * KW + v][16 * (m >> 2) + t][m & 3];
+                if (p.slices == 1)
+                    gemv_store<F>(p, unit, m, t, sum);
+                else if (t < T)
+                    *MOE_CHECKED(p.part + (((size_t)unit * p.slices + slice) * T + t) * 16 + m, 4, p.part,
+                                 (size_t)p.units * p.slices * T * 64) = sum;
+            }
         }
+        __syncthreads();
     }
     if (p.slices == 1) return;
     // the last workgroup of the range adds the slices (their stores complete
@@ -188,30 +268,53 @@ __global__ __launch_bounds__(kGemvThreads) void gemv_w4_kernel(GemvArgs p) {
         __threadfence();
         const bool last = atomicInc(p.ctr + range, p.slices - 1) == (uint32_t)p.slices - 1;
         if (last) __threadfence();
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the invalidation is complete before the others load
         sm.last = last;
     }
     __syncthreads();
-    if (!sm.last || threadIdx.x >= 256) return;
-    const int m = threadIdx.x & 15, t = threadIdx.x >> 4;
-    for (int u = u0; u < u1; ++u) {
+    if (!uniform(sm.last)) return;
+    for (int i = wave; i < 4 * (u1 - u0); i += kGemvWaves) {
+        const int unit = u0 + (i >> 2), m = lane & 15, t = 4 * (i & 3) + (lane >> 4);
+        if (4 * (i & 3) >= T) continue;
         float sum = 0.f;
         for (int s = 0; t < T && s < p.slices; ++s)
-            sum += *MOE_CHECKED(p.part + (((size_t)u * p.slices + s) * T + t) * 16 + m, 4, p.part,
+            sum += *MOE_CHECKED(p.part + (((size_t)unit * p.slices + s) * T + t) * 16 + m, 4, p.part,
                                 (size_t)p.units * p.slices * T * 64);
-        gemv_store<F>(p, u, m, t, sum);
+        gemv_store<F>(p, unit, m, t, sum);
     }
+}
+
+// Steps in a ring: the deep one where it leaves the token rows room, else the
+// shallow one.
+constexpr int kGemvDeep = 6, kGemvShallow = 3;
+
+// LDS bytes that `steps` steps of token rows (and INT4's token sums) take.
+size_t gemv_x_bytes(int T, int steps) { return (size_t)steps * 512 * T + (size_t)steps * 32 * T; }
+size_t gemv_ring_bytes(int slot, int s) { return (size_t)kGemvWaves * s * slot; }
+
+template <int F, int GROUP, bool ZEROS>
+void launch_format(const GemvArgs &p, hipStream_t st) {
+    constexpr int slot = GemvSlot<F, GROUP, ZEROS>::SLOT;
+    const dim3 grid(p.ranges * p.slices), block(kGemvThreads);
+    const int steps = (few_steps(F, p.K) + p.slices - 1) / p.slices;
+    if (gemv_x_bytes(p.T, steps) + gemv_ring_bytes(slot, kGemvDeep) <= (size_t)kGemvArea)
+        gemv_w4_kernel<F, GROUP, ZEROS, kGemvDeep><<<grid, block, 0, st>>>(p);
+    else
+        gemv_w4_kernel<F, GROUP, ZEROS, kGemvShallow><<<grid, block, 0, st>>>(p);
 }
 
 }  // namespace
 
-// Workgroups of a product: `ranges` of units times `slices` of K.  The slices
-// are as many as the token rows need to fit the LDS.
-GemvPlan gemv_plan(int T, int N, int K, bool geglu) {
+// Workgroups of a product: `ranges` of units times `slices` of K, as many
+// slices as the token rows need to fit the LDS next to the shallow ring.
+GemvPlan gemv_plan(GemvFormat fmt, int group, bool zeros, int T, int N, int K, bool geglu) {
     GemvPlan g;
     g.outs = geglu ? N / 2 : N;
     g.units = geglu ? (g.outs + 7) / 8 : (N - 1) / 16 + 1;
-    const int blocks = (K - 1) / 128 + 1, fit = kGemvXBytes / (256 * T);
-    g.slices = (blocks + fit - 1) / fit;
+    const int steps = (K - 1) / 256 + 1;
+    const int words = fmt == GemvFormat::kINT4 ? (group == 32 ? 2 : 1) * (zeros ? 2 : 1) : 2;
+    const int fit = (int)((kGemvArea - gemv_ring_bytes(2048 + 256 * words, kGemvShallow)) / gemv_x_bytes(T, 1));
+    g.slices = (steps + fit - 1) / fit;
     g.ranges = std::min(g.units, std::max(1, kGemvBlocks / g.slices));
     return g;
 }
@@ -221,7 +324,7 @@ size_t gemv_part_bytes(const GemvPlan &g, int T) {
 }
 
 hipError_t launch_gemv_w4(const GemvW4 &l, hipStream_t st) {
-    const GemvPlan g = gemv_plan(l.T, l.N, l.K, l.geglu);
+    const GemvPlan g = gemv_plan(l.fmt, l.group, l.zeros != nullptr, l.T, l.N, l.K, l.geglu);
     GemvArgs p{};
     p.x = l.x;
     p.w = l.w;
@@ -243,12 +346,11 @@ hipError_t launch_gemv_w4(const GemvW4 &l, hipStream_t st) {
     p.slices = g.slices;
     p.geglu = l.geglu;
     p.y_fp32 = l.y_fp32;
-    const dim3 grid(g.ranges * g.slices), block(kGemvThreads);
-    if (l.fmt == GemvFormat::kMXFP4) gemv_w4_kernel<kFewMx, 0><<<grid, block, 0, st>>>(p);
-    else if (l.fmt == GemvFormat::kNVFP4) gemv_w4_kernel<kFewNv, 0><<<grid, block, 0, st>>>(p);
-    else if (l.group == 32) gemv_w4_kernel<kFewI4, 32><<<grid, block, 0, st>>>(p);
-    else if (l.group == 64) gemv_w4_kernel<kFewI4, 64><<<grid, block, 0, st>>>(p);
-    else gemv_w4_kernel<kFewI4, 128><<<grid, block, 0, st>>>(p);
+    if (l.fmt == GemvFormat::kMXFP4) launch_format<kFewMx, 0, false>(p, st);
+    else if (l.fmt == GemvFormat::kNVFP4) launch_format<kFewNv, 0, false>(p, st);
+    else if (l.group == 32) l.zeros ? launch_format<kFewI4, 32, true>(p, st) : launch_format<kFewI4, 32, false>(p, st);
+    else if (l.group == 64) l.zeros ? launch_format<kFewI4, 64, true>(p, st) : launch_format<kFewI4, 64, false>(p, st);
+    else l.zeros ? launch_format<kFewI4, 128, true>(p, st) : launch_format<kFewI4, 128, false>(p, st);
     return hipGetLastError();
 }
 

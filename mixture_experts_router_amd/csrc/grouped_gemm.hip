@@ -287,31 +287,6 @@ __device__ __forceinline__ void wait_vm_lgkm0_rt(int n) {
     }
 }
 
-// 16-byte direct global->LDS load of one wave: lane l's 16 bytes from `g`
-// land at lds + 16 l.  Issued from inline asm so that the compiler adds no
-// waits of its own on later LDS reads (it cannot tell the stage buffers
-// apart); every wait is the explicit s_waitcnt of the pipeline below.  The
-// asm has no register outputs, and M0 is only ever set here.
-// STREAM sets the non-temporal hint, for data read exactly once: on gfx950 a
-// streaming read of whole lines with the hint reaches about 10% more HBM
-// bandwidth (measured: 6.8 vs 6.1 TB/s for a 2 GiB read).  Data that other
-// workgroups re-read, or lines consumed in pieces over several K steps (the
-// 32-byte MXFP4 row slices), lose more from the early eviction than they gain.
-// The compiler reserves M0 and ignores it in a clobber list (it warns so);
-// nothing it generates in these kernels keeps a value in M0 (no LDS-DMA,
-// GWS, message or relative-move builtins are used), so setting it inside
-// the asm is safe, and the warning is silenced for these two helpers.
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-template <bool STREAM>
-__device__ __forceinline__ void dma16(const void *g, const void *lds) {
-    const uint32_t l = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds);
-    if (STREAM)
-        asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off nt" ::"v"(g), "s"(l) : "memory", "m0");
-    else
-        asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(g), "s"(l) : "memory", "m0");
-}
-
 // Epilogue exchange between lanes l and l ^ 16 (k groups lk and lk ^ 1, which
 // hold columns 4 lk .. 4 lk + 3 of the same output row): a lane of an even
 // group keeps fragment 0's four values and receives its partner's, a lane of
@@ -328,14 +303,6 @@ __device__ __forceinline__ uint4 pair_swap16(uint2 f0, uint2 f1, int odd) {
     const uint2 recv = odd ? make_uint2(rx[0], ry[0]) : make_uint2(rx[1], ry[1]);
     return odd ? make_uint4(recv.x, recv.y, keep.x, keep.y) : make_uint4(keep.x, keep.y, recv.x, recv.y);
 }
-
-// 4-byte direct global->LDS load of one wave: lane l's 4 bytes from `g`
-// land at lds + 4 l (same rules as dma16).
-__device__ __forceinline__ void dma4(const void *g, const void *lds) {
-    const uint32_t l = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds);
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" ::"v"(g), "s"(l) : "memory", "m0");
-}
-#pragma clang diagnostic pop
 
 template <int BM, int BN, int WAVES_M, int WAVES_N, int MODE, bool MX, int NS_, int BK_, bool A4 = false,
           bool NV = false, bool WD = false, int NSB_ = 0>

@@ -146,6 +146,39 @@ __device__ __forceinline__ f32x4 mfma16x16x32(const u32x4 &a, const u32x4 &b, f3
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, bv, c, 0, 0, 0);
 }
 
+// 16-byte direct global->LDS load of one wave: lane l's 16 bytes from `g`
+// land at lds + 16 l.  Issued from inline asm so that the compiler adds no
+// waits of its own on later LDS reads (it cannot tell the stage buffers
+// apart); every wait is the explicit s_waitcnt of the pipeline that uses it.  The
+// asm has no register outputs, and M0 is only ever set here.
+// STREAM sets the non-temporal hint, for data read exactly once: on gfx950 a
+// streaming read of whole lines with the hint reaches about 10% more HBM
+// bandwidth (measured: 6.8 vs 6.1 TB/s for a 2 GiB read).  Data that other
+// workgroups re-read, or lines consumed in pieces over several K steps (the
+// 32-byte MXFP4 row slices), lose more from the early eviction than they gain.
+// The compiler reserves M0 and ignores it in a clobber list (it warns so);
+// nothing it generates in these kernels keeps a value in M0 (no LDS-DMA,
+// GWS, message or relative-move builtins are used), so setting it inside
+// the asm is safe, and the warning is silenced for these two helpers.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+template <bool STREAM>
+__device__ __forceinline__ void dma16(const void *g, const void *lds) {
+    const uint32_t l = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds);
+    if (STREAM)
+        asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off nt" ::"v"(g), "s"(l) : "memory", "m0");
+    else
+        asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(g), "s"(l) : "memory", "m0");
+}
+
+// 4-byte direct global->LDS load of one wave: lane l's 4 bytes from `g`
+// land at lds + 4 l (same rules as dma16).
+__device__ __forceinline__ void dma4(const void *g, const void *lds) {
+    const uint32_t l = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds);
+    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" ::"v"(g), "s"(l) : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
 // gelu_pytorch_tanh: 0.5 z (1 + tanh(u)), u = sqrt(2/pi) (z + 0.044715 z^3),
 // evaluated as z / (1 + exp(-2u)) (the same function: 0.5 (1 + tanh u) is
 // the logistic function of 2u).  Large |u| saturates to z or -0.

@@ -67,6 +67,7 @@ def test_few_arguments(lib):
     assert few(lib, S(), gus=F) == -1                                     # bf16 weights come without scales
     assert few(lib, S(f=1)) == -1                                         # MXFP4 weights need them
     assert few(lib, S(f=1), gus=F, ds=F, gu=F + 4) == -1                  # 4-bit codes 16-byte aligned
+    assert few(lib, S(f=1), gus=MIS, ds=F) == -1                          # scales 4-byte aligned
     assert few(lib, S(f=3), gus=F, ds=MIS) == -1                          # NVFP4 scale buffers 4-byte aligned
     assert few(lib, S(), I_sh=-64) == -1
     assert few(lib, S(), I_sh=100, sgu=F, sd=F) == -2
@@ -99,6 +100,7 @@ def test_gemv_arguments(lib):
     assert gemv(lib, W(), x=F + 8) == -1 and gemv(lib, W(), w=F + 8) == -1 and gemv(lib, W(), scales=F + 1) == -1
     assert gemv(lib, W(), y=F + 1) == -1 and gemv(lib, W(flags=2), y=MIS) == -1 and gemv(lib, W(), bias=MIS) == -1
     assert gemv(lib, W(f=3, group=0), scales=MIS) == -1
+    assert gemv(lib, W(), scales=MIS) == -1 and gemv(lib, W(), zeros=MIS) == -1 and gemv(lib, W(f=1, group=0), scales=MIS) == -1
     assert gemv(lib, W(f=1, group=0), zeros=F) == -1 and gemv(lib, W(f=3, group=0), zeros=F) == -1
     # token rows too long for one workgroup: partial sums, so a workspace
     s = W(T=16, K=1 << 16)
