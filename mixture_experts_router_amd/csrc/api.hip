@@ -157,6 +157,7 @@ struct FewWorkspace {
     uint32_t *counters;
     float *logits;
     uint16_t *h, *h_sh;
+    float *y;
     size_t bytes;
 };
 
@@ -173,6 +174,7 @@ FewWorkspace carve_few(const moe_shape *s, void *base, int I_sh) {
     w.logits = reinterpret_cast<float *>(take((size_t)s->T * s->E * sizeof(float)));
     w.h = reinterpret_cast<uint16_t *>(take((size_t)s->T * s->k * s->I * sizeof(uint16_t)));
     w.h_sh = I_sh > 0 ? reinterpret_cast<uint16_t *>(take((size_t)s->T * I_sh * sizeof(uint16_t))) : nullptr;
+    w.y = reinterpret_cast<float *>(take(moe::few_layer_y(weight_view(s, nullptr).fmt, s->T, s->H, s->k, s->I, I_sh)));
     w.bytes = off;
     return w;
 }
@@ -599,6 +601,7 @@ int moe_forward_few(const moe_shape *s, const uint16_t *x, const uint16_t *w_rou
     l.logits = w.logits;
     l.h = w.h;
     l.h_sh = w.h_sh;
+    l.y = w.y;
     l.T = s->T;
     l.H = s->H;
     l.E = s->E;

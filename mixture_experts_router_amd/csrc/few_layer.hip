@@ -34,9 +34,14 @@ constexpr int kFewWaves = 8, kFewThreads = 64 * kFewWaves;
 constexpr int kFewMaxA = kFewTokens * 32;                 // assignments (k <= 32)
 constexpr int kFewArea = 136 * 1024;                      // LDS for the rings and the token rows
 
-// Counters in the workspace's zeroed prefix, a line each.
-constexpr int kCtrRouterTicket = 0, kCtrGateUpTicket = 32, kCtrDownTicket = 64;   // next item of each phase
-constexpr int kCtrRouter = 96, kCtrGateUp = 128, kCtrExit = 160;                    // items done, workgroups left
+// Counters in the workspace's zeroed prefix, a line each: tickets (the next
+// item of each phase), items done, workgroups left.  A phase's items done are
+// counted in one place and, when all are, signalled in kSignals: 256 workgroups
+// polling the count itself hold up each other and those that still count.
+enum FewPhase { kRouter = 0, kGateUp = 1, kDown = 2, kCombine = 3 };
+constexpr int kCtrTicket = 0, kCtrDone = 4, kCtrExit = 7, kCtrSignal = 8, kSignals = 8;
+constexpr int kCtrLine = 32, kCtrWords = kCtrLine * (kCtrSignal + 3 * kSignals);
+static_assert(kCtrWords * 4 == kFewCounterBytes, "the zeroed prefix");
 
 struct FewArgs {
     const uint16_t *x, *wr;
@@ -51,8 +56,10 @@ struct FewArgs {
     uint32_t *ctr;
     float *logits;
     uint16_t *h, *h_sh;                         // [T k][I], [T][I_sh]
+    float *y;                                   // [segment of an expert][T k][H], [segment of the MLP][T][H]
     int T, H, E, k, I, I_sh;
-    int n_router, n_gu, n_down;                 // items of each phase
+    int n_router, n_gu, n_down, n_combine;      // items of each phase
+    int columns, PW, ne, ns;                    // down: see FewDown, FewPieces
 };
 
 struct FewSmem {
@@ -83,23 +90,35 @@ __device__ __forceinline__ void store_shared(V *p, V v) {
     __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// Counts this workgroup's stored results: every wave's stores are complete,
-// then one thread counts.
-__device__ __forceinline__ void publish(uint32_t *done) {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    if (threadIdx.x == 0) ctr_add(done);
+__device__ __forceinline__ uint32_t ctr_ticket(const FewArgs &p, FewPhase phase) {
+    return ctr_add(p.ctr + kCtrLine * (kCtrTicket + phase));
 }
 
-// One thread waits until `n` workgroups have published; its workgroup, which
+// One thread counts an item of a phase of n done: its workgroup's stores are complete.
+__device__ __forceinline__ void ctr_done(const FewArgs &p, FewPhase phase, int n) {
+    if (ctr_add(p.ctr + kCtrLine * (kCtrDone + phase)) != (uint32_t)n - 1) return;
+#pragma unroll
+    for (int i = 0; i < kSignals; ++i) store_shared(p.ctr + kCtrLine * (kCtrSignal + kSignals * phase + i), 1u);
+}
+
+// Counts this workgroup's stored results: every wave's stores are complete,
+// then one thread counts.
+__device__ __forceinline__ void publish(const FewArgs &p, FewPhase phase, int n) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (threadIdx.x == 0) ctr_done(p, phase, n);
+}
+
+// One thread waits until all items of a phase are done; its workgroup, which
 // joins a barrier next, may then load what they stored: the caches'
 // invalidation is complete, not merely requested, before the others load.
-// The count is reached as long as the counters were zero before the launch;
+// The signal comes as long as the counters were zero before the launch;
 // the bound only keeps a workspace that was not from holding the GPU (its
 // results are then undefined).
-__device__ __forceinline__ void wait_count(uint32_t *ctr, uint32_t n) {
+__device__ __forceinline__ void wait_done(const FewArgs &p, FewPhase phase) {
+    const uint32_t *flag = p.ctr + kCtrLine * (kCtrSignal + kSignals * phase + blockIdx.x % kSignals);
     for (int i = 0; i < (1 << 20); ++i) {
-        if (__hip_atomic_load(ctr, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) >= n) break;
+        if (__hip_atomic_load(flag, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) break;
         __builtin_amdgcn_s_sleep(1);
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
@@ -202,7 +221,7 @@ __device__ void few_select(const FewArgs &p, FewSmem &sm, bool store) {
     const int wave = wave_index(), A = p.T * p.k, a = threadIdx.x;
     for (int i = threadIdx.x; i < A * kFewTokens / 4; i += kFewThreads) reinterpret_cast<uint32_t *>(sm.slot)[i] = 0u;
     if (threadIdx.x < 32) sm.mask[threadIdx.x] = 0u;
-    if (threadIdx.x == 0) wait_count(p.ctr + kCtrRouter, p.n_router);
+    if (threadIdx.x == 0) wait_done(p, kRouter);
     __syncthreads();
     for (int t = wave; t < p.T; t += kFewWaves) {
         if (p.E <= 64) few_topk<1>(p, sm, t, store);
@@ -251,18 +270,6 @@ __device__ void few_select(const FewArgs &p, FewSmem &sm, bool store) {
 }
 
 // ---------------------------------------------------------------- gate/up
-// The token operand of MFMA f, lane (r, g): from LDS, where every fragment
-// has 16 bytes per (g, token), or from the rows of x.
-template <int F, bool XL>
-__device__ __forceinline__ u32x4 few_x_frag(const FewArgs &p, const uint8_t *xs, int f, int r, int g) {
-    const int t = min(r, p.T - 1);
-    if constexpr (XL) return *reinterpret_cast<const u32x4 *>(xs + 64 * f * p.T + (g * p.T + t) * 16);
-    const int k = few_frag_k<F>(f, g);
-    u32x4 v = *reinterpret_cast<const u32x4 *>(
-        MOE_CHECKED(p.x + (size_t)t * p.H + (k < p.H ? k : 0), 16, p.x, (size_t)p.T * p.H * 2));
-    return k < p.H ? v : u32x4{0u, 0u, 0u, 0u};
-}
-
 template <int F>
 __device__ void few_stage_x(const FewArgs &p, uint8_t *xs) {
     const int nfrag = few_steps(F, p.H) * FewStep<F>::FRAGS;
@@ -276,320 +283,420 @@ __device__ void few_stage_x(const FewArgs &p, uint8_t *xs) {
     __syncthreads();
 }
 
-// Units u0 .. u1 - 1 of eight h columns: the MFMA's rows are the unit's eight
-// gate rows and the matching eight up rows.  The workgroup takes 8 / KW units
-// at a time, KW waves splitting the K of each.
-template <int F, int S, bool XL>
-__device__ __forceinline__ void few_gateup(const FewArgs &p, FewSmem &sm, bool shared, int u0, int u1) {
-    constexpr int SLOT = FewStep<F>::SLOT, OPS = FewStep<F>::OPS, FRAGS = FewStep<F>::FRAGS;
-    const int lane = threadIdx.x & 63, wave = wave_index(), r = lane & 15, g = lane >> 4;
-    const int I = shared ? p.I_sh : p.I, H = p.H, per = I / 8;
-    if (u0 >= u1) return;
-    const int ns = few_steps(F, H), KW = few_kwaves(u1 - u0, ns), UG = kFewWaves / KW;
-    const int kw = wave % KW, s0 = kw * ns / KW, s1 = (kw + 1) * ns / KW;
-    const uint8_t *w = shared ? p.swgu : p.wgu, *s = shared ? p.sgus : p.gus;
-    const FewLane<F> ln(H);
-    const size_t wn = (size_t)(shared ? 1 : p.E) * 2 * I * ln.pitch, sn = (size_t)(shared ? 1 : p.E) * 2 * I * ln.spitch;
-    // (a unit's scale rows start at a multiple of 4 bytes)
-    const uint32_t lo = (ln.r & 7) * ln.spitch;
-    uint8_t *ring = sm.area + wave * S * SLOT;
-    const uint8_t *xs = sm.area + kFewWaves * S * SLOT;
+// A workgroup's run of units, each an MFMA tile of sixteen weight rows summed
+// along its steps.  Whole rounds of eight units go a unit to a wave and need no
+// barrier; the units that are left (fewer than eight) are split along K so that
+// no wave is longer at work than it must, and their sums joined.  The order of
+// each unit's sum depends on the run alone.
+//
+// Src says what the units are: at(u, v) (its segment of the weights, v or a
+// later one), lane(v) (the row length), span(v, a, b) (its steps), rows(u, v),
+// operand(v) (this lane's token data), frag(operand, step, i), finish(u, v,
+// sums).
+template <int F, int S, class Src>
+struct FewUnits {
+    static constexpr int SLOT = FewStep<F>::SLOT, OPS = FewStep<F>::OPS, FRAGS = FewStep<F>::FRAGS;
+    const Src &src;
+    FewSmem &sm;
+    uint8_t *ring;
+    int wave, lane;
+    int u0 = 0, um = 0, u1 = 0, KW = 1, UG = 1;      // the run; um: the units that are left, UG at a time
+    int v0 = 0;                                       // its first segment
+    int lu = 0, lv = 0, ls = 0, ls1 = 0, lslot = 0;   // the step to request next (u1: none) and its slot
+    FewRows rows;
 
-    // the step to request next: of unit lu, and where that unit's rows are
-    int lu = u0 + wave / KW, ls = s0, lslot = 0;
-    FewRows<F> rows;
-    auto point = [&]() {
-        const int ue = lu / per;
-        const size_t row = (size_t)(shared ? 0 : uniform(sm.expert[ue])) * 2 * I + 8 * (lu - ue * per);
-        rows.top = w + row * ln.pitch;
-        rows.low = rows.top + (size_t)I * ln.pitch;
-        rows.stop = s + row * ln.spitch;
-        rows.slow = rows.stop + (size_t)I * ln.spitch;
-    };
-    auto request = [&]() {
-        ln.issue(rows, ls, ring + lslot * SLOT, w, wn, s, sn);
-        lslot = lslot + 1 == S ? 0 : lslot + 1;
-        if (++ls == s1) {
-            ls = s0;
-            lu += UG;
-            if (lu < u1) point();
+    __device__ __forceinline__ FewUnits(const Src &src, FewSmem &sm)
+        : src(src), sm(sm), wave(wave_index()), lane(threadIdx.x & 63) {
+        ring = sm.area + wave * S * SLOT;
+    }
+    // this wave's steps of unit u of segment v
+    __device__ __forceinline__ void part(int u, int v, int &a, int &b) const {
+        src.span(v, a, b);
+        if (u >= um) {
+            const int kw = wave & (KW - 1), n = b - a;
+            b = a + (kw + 1) * n / KW;
+            a += kw * n / KW;
         }
-    };
-    if (s0 == s1) lu = u1;   // more waves than steps
-    if (lu < u1) {
-        point();
+    }
+    // the next unit with steps for this wave: u, or one after it (left: u is one of the units that are left)
+    __device__ __forceinline__ void seek(int u, bool left) {
+        for (;; u += left ? UG : kFewWaves) {
+            if (!left && u >= um) {
+                left = true;
+                u = um + wave / KW;
+            }
+            lu = u1;
+            if (u >= u1) return;
+            lv = src.at(u, lv);
+            part(u, lv, ls, ls1);
+            if (ls < ls1) break;   // not where there are more waves than steps
+        }
+        lu = u;
+        rows = src.rows(u, lv);
+    }
+    __device__ __forceinline__ void request() {
+        src.lane(lv).issue(rows, ls, ring + lslot * SLOT, src.weights(lv), src.weight_bytes(lv), src.scales(lv),
+                           src.scale_bytes(lv));
+        lslot = lslot + 1 == S ? 0 : lslot + 1;
+        if (++ls == ls1) seek(lu + (lu >= um ? UG : kFewWaves), lu >= um);
+    }
+    // Requests the first steps of units a .. b - 1, a of segment v, each of at most `steps` steps.
+    __device__ __forceinline__ void start(int a, int b, int v, int steps) {
+        u0 = a;
+        u1 = b;
+        um = b - (b - a) % kFewWaves;
+        KW = few_kwaves(b - um, steps);
+        UG = kFewWaves / KW;
+        v0 = lv = v;
+        lslot = 0;
+        seek(u0 + wave, false);
         for (int i = 0; i < S && lu < u1; ++i) request();
     }
-    int slot = 0;
-    for (int v0 = u0; v0 < u1; v0 += UG) {
-        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-        if (uniform(v0 + wave / KW < u1)) {
-            for (int st = s0; st < s1; ++st) {
-                const uint8_t *q = ring + slot * SLOT;
-                // the ring is full but for this step's successors: S - 1 steps may be in flight
-                if (uniform(lu < u1)) few_wait<(S - 1) * OPS>();
-                else few_wait<0>();
-                if constexpr (F == kFewBf16) {
+    __device__ __forceinline__ void run() {
+        int slot = 0, v = v0;
+        for (int i = u0; i < u1;) {
+            const bool left = i >= um;
+            const int u = i + (left ? wave / KW : wave);
+            f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+            if (uniform(u < u1)) {
+                v = src.at(u, v);
+                const auto ln = src.lane(v);
+                const auto x = src.operand(v);
+                // (a unit's scale rows start at a multiple of 4 bytes)
+                [[maybe_unused]] const uint32_t lo = (ln.r & 7) * ln.spitch;
+                int a, b;
+                part(u, v, a, b);
+                for (int st = a; st < b; ++st) {
+                    const uint8_t *q = ring + slot * SLOT;
+                    // the ring is full but for this step's successors: S - 1 steps may be in flight
+                    if (lu < u1) few_wait<(S - 1) * OPS>();
+                    else few_wait<0>();
+                    // everything of the step into registers at once, then its slot is free for another
+                    const u32x4 c[2] = {ln.load(q, 0), ln.load(q, 1)};
+                    [[maybe_unused]] uint32_t sc[2];
+                    if constexpr (FewStep<F>::SOPS > 0) {
+                        sc[0] = ln.scale(q, st, 0, lo);
+                        sc[1] = ln.scale(q, st, 1, lo);
+                    }
+                    u32x4 xf[FRAGS];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        acc = mfma16x16x32(ln.load(q, i), few_x_frag<F, XL>(p, xs, st * FRAGS + i, r, g), acc);
-                } else {
+                    for (int f = 0; f < FRAGS; ++f) xf[f] = src.frag(x, st, f);
+                    few_lds_done();
+                    if (lu < u1) request();
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const u32x4 c = ln.load(q, h);
-                        const uint32_t sc = ln.scale(q, st, h, lo);
+                        if constexpr (F == kFewBf16) {
+                            acc[h] = mfma16x16x32(c[h], xf[h], acc[h]);
+                        } else {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            acc = mfma16x16x32(few_operand<F>(c, sc, i),
-                                               few_x_frag<F, XL>(p, xs, st * FRAGS + 4 * h + i, r, g), acc);
+                            for (int f = 0; f < 4; ++f)
+                                acc[h] = mfma16x16x32(few_operand<F>(c[h], sc[h], f), xf[4 * h + f], acc[h]);
+                        }
                     }
+                    slot = slot + 1 == S ? 0 : slot + 1;
                 }
-                few_lds_done();
-                if (uniform(lu < u1)) request();
-                slot = slot + 1 == S ? 0 : slot + 1;
             }
+            const f32x4 sum = acc[0] + acc[1];
+            if (!left) {
+                src.finish(u, v, sum);
+            } else {
+                sm.red[wave][lane] = sum;
+                __syncthreads();
+                if (uniform(wave < UG && i + wave < u1)) {
+                    f32x4 all = {0.f, 0.f, 0.f, 0.f};
+                    for (int w = 0; w < KW; ++w) all += sm.red[wave * KW + w][lane];
+                    src.finish(i + wave, src.at(i + wave, v0), all);
+                }
+                __syncthreads();
+            }
+            i += left ? UG : kFewWaves;
         }
-        sm.red[wave][lane] = acc;
-        __syncthreads();
-        // wave v finishes unit v0 + v: lane 4 t + i has token t and columns 2i, 2i + 1.  Lane 16 (m / 4) + t,
-        // element m % 4 of each wave's sums is weight row m, token t: gate rows 0..7, up rows 8..15
-        const int u = v0 + wave;
-        if (uniform(wave < UG && u < u1)) {
-            const int i = 2 * (lane & 3), t = lane >> 2, ue = u / per;
-            float gate[2] = {0.f, 0.f}, up[2] = {0.f, 0.f};
-            for (int v = 0; v < KW; ++v) {
-                const float *a = reinterpret_cast<const float *>(&sm.red[wave * KW + v][16 * (i >> 2) + t]) + (i & 3);
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    gate[q] += a[q];
-                    up[q] += a[4 * 32 + q];
-                }
-            }
-            if constexpr (F == kFewNv) {
-                const float m = shared ? p.sgug[0] : p.gug[uniform(sm.expert[ue])];
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    gate[q] *= m;
-                    up[q] *= m;
-                }
-            }
-            const uint32_t hv = pack_bf16x2(gelu_tanh(gate[0]) * up[0], gelu_tanh(gate[1]) * up[1]);
-            const int j = t < p.T ? (shared ? 1 : (int)sm.slot[ue][t]) : 0;
-            if (j) {
-                uint16_t *base = shared ? p.h_sh : p.h;
-                const size_t row = shared ? (size_t)t : (size_t)t * p.k + j - 1;
-                store_shared(reinterpret_cast<uint32_t *>(MOE_CHECKED(base + row * I + 8 * (u - ue * per) + i, 4, base,
-                                                                      (size_t)p.T * (shared ? 1 : p.k) * I * 2)), hv);
-            }
-        }
-        __syncthreads();
-    }
-}
-
-// ---------------------------------------------------------------- down
-// Sixteen output columns per item, summed over sub-units: the touched experts
-// (or K pieces of them, where sixteen of their rows do not fit the LDS), then
-// the dense MLP in pieces of the same size.  The waves take sub-units in turn
-// and their sums are added in wave order.  h is staged in LDS for as many
-// sub-units as fit (a pass); the ring's first weights of a pass are requested
-// before its h is staged, those of the first one before h exists.
-template <int F, int S>
-struct FewPieces {
-    // LDS for rows of h, and the largest piece of which sixteen fit
-    static constexpr int H_BYTES = kFewArea - kFewWaves * S * FewStep<F>::SLOT;
-    static constexpr int MAX = (H_BYTES / kFewTokens - 16) / (FewStep<F>::K * 2);
-    static_assert(MAX >= 1, "one step of sixteen rows fits");
-    int PW, pitch, ne, ns, U, T, A, n;   // steps of a piece, bytes of a row of it, pieces of an expert, of the MLP
-    __device__ __forceinline__ FewPieces(const FewArgs &p, int n_experts) {
-        const int st = few_steps(F, p.I), want = (st + MAX - 1) / MAX;
-        PW = (st + want - 1) / want;
-        pitch = PW * FewStep<F>::K * 2 + 16;
-        ne = (st + PW - 1) / PW;
-        ns = p.I_sh ? (few_steps(F, p.I_sh) + PW - 1) / PW : 0;
-        U = n_experts;
-        T = p.T;
-        A = p.T * p.k;
-        n = U * ne + ns;
-    }
-    // rows of h of the sub-units before v
-    __device__ __forceinline__ int rows_before(const FewSmem &sm, int v) const {
-        if (v >= U * ne) return A * ne + (v - U * ne) * T;
-        const int e = v / ne, q = v - e * ne, f = sm.first[e];
-        return f * ne + q * (sm.first[e + 1] - f);
     }
 };
 
-template <int F, int S>
-__device__ __forceinline__ void few_down_items(const FewArgs &p, FewSmem &sm, int item) {
-    constexpr int SLOT = FewStep<F>::SLOT, OPS = FewStep<F>::OPS, FRAGS = FewStep<F>::FRAGS, KS = FewStep<F>::K;
-    using P = FewPieces<F, S>;
-    const int lane = threadIdx.x & 63, wave = wave_index(), r = lane & 15, g = lane >> 4;
-    const P pc(p, uniform(sm.n_experts));
-    const int UE = pc.U * pc.ne;
-    uint8_t *ring = sm.area + wave * S * SLOT;
-    uint8_t *hs = sm.area + kFewWaves * S * SLOT;
+// Gate/up units of eight h columns: the MFMA's rows are the unit's eight gate
+// rows and the matching eight up rows.
+template <int F, int S, bool XL>
+struct FewGateUp {
+    const FewArgs &p;
+    FewSmem &sm;
+    const bool shared;
+    const int I, per;          // units of an expert
+    const FewLane<F> ln;
 
-    int va = 0, vb = 0;              // the pass: sub-units va .. vb - 1
-    int lv = 0, ls = 0, ls1 = 0, lslot = 0;   // next step to request: of sub-unit lv
-    FewRows<F> rows;
-    auto steps = [&](int v, int &a, int &b) {   // steps [a, b) of its row that sub-unit v covers
-        const int q = v < UE ? v % pc.ne : v - UE;
-        a = q * pc.PW;
-        b = min(few_steps(F, v < UE ? p.I : p.I_sh), a + pc.PW);
-    };
-    auto point = [&]() {
-        const bool mlp = lv >= UE;
-        const size_t row = (size_t)(mlp ? 0 : uniform(sm.expert[lv / pc.ne])) * p.H + 16 * item;
-        const FewLane<F> ln(mlp ? p.I_sh : p.I);
-        rows.top = (mlp ? p.swd : p.wd) + row * ln.pitch;
-        rows.low = rows.top + (size_t)8 * ln.pitch;
-        rows.stop = (mlp ? p.sds : p.ds) + row * ln.spitch;
-        rows.slow = rows.stop + (size_t)8 * ln.spitch;
-        steps(lv, ls, ls1);
-    };
-    auto request = [&]() {
-        uint8_t *q = ring + lslot * SLOT;
-        const bool mlp = lv >= UE;
-        const FewLane<F> ln(mlp ? p.I_sh : p.I);
-        const size_t nr = (size_t)(mlp ? 1 : p.E) * p.H;
-        ln.issue(rows, ls, q, mlp ? p.swd : p.wd, nr * ln.pitch, mlp ? p.sds : p.ds, nr * ln.spitch);
-        lslot = lslot + 1 == S ? 0 : lslot + 1;
-        if (++ls == ls1) {
-            lv += kFewWaves;
-            if (lv < vb) point();
+    __device__ __forceinline__ FewGateUp(const FewArgs &p, FewSmem &sm, bool shared)
+        : p(p), sm(sm), shared(shared), I(shared ? p.I_sh : p.I), per(I / 8), ln(p.H) {}
+    __device__ __forceinline__ int at(int u, int v) const {   // (segment: touched expert)
+        while (u >= (v + 1) * per) ++v;
+        return v;
+    }
+    __device__ __forceinline__ const FewLane<F> &lane(int) const { return ln; }
+    __device__ __forceinline__ const uint8_t *weights(int) const { return shared ? p.swgu : p.wgu; }
+    __device__ __forceinline__ const uint8_t *scales(int) const { return shared ? p.sgus : p.gus; }
+    __device__ __forceinline__ size_t weight_bytes(int) const { return (size_t)(shared ? 1 : p.E) * 2 * I * ln.pitch; }
+    __device__ __forceinline__ size_t scale_bytes(int) const { return (size_t)(shared ? 1 : p.E) * 2 * I * ln.spitch; }
+    __device__ __forceinline__ void span(int, int &a, int &b) const {
+        a = 0;
+        b = few_steps(F, p.H);
+    }
+    __device__ __forceinline__ FewRows rows(int u, int v) const {
+        const size_t row = (size_t)(shared ? 0 : uniform(sm.expert[v])) * 2 * I + 8 * (u - v * per);
+        const uint8_t *w = weights(v) + row * ln.pitch, *s = scales(v) + row * ln.spitch;
+        return ln.rows(w, w + (size_t)I * ln.pitch, s, s + (size_t)I * ln.spitch);
+    }
+    // XL: the token rows are in LDS, every fragment as 16 bytes per (g, token)
+    __device__ __forceinline__ const uint8_t *operand(int) const {
+        const int t = min((int)ln.r, p.T - 1);
+        if constexpr (XL) return sm.area + kFewWaves * S * FewStep<F>::SLOT + (ln.g * p.T + t) * 16;
+        return reinterpret_cast<const uint8_t *>(p.x + (size_t)t * p.H);
+    }
+    __device__ __forceinline__ u32x4 frag(const uint8_t *x, int st, int i) const {
+        const int f = st * FewStep<F>::FRAGS + i;
+        if constexpr (XL) return *reinterpret_cast<const u32x4 *>(x + 64 * f * p.T);
+        const int k = few_frag_k<F>(f, ln.g);
+        const u32x4 v =
+            *reinterpret_cast<const u32x4 *>(MOE_CHECKED(x + 2 * (k < p.H ? k : 0), 16, p.x, (size_t)p.T * p.H * 2));
+        return k < p.H ? v : u32x4{0u, 0u, 0u, 0u};
+    }
+    // Lane 16 g + t, element q of the sums is weight row 4 g + q, token t: gate rows 0..7, up rows 8..15, so a
+    // gate's up value is 32 lanes above.
+    __device__ __forceinline__ void finish(int u, int v, const f32x4 &acc) const {
+        const int t = ln.r;
+        const float m = F != kFewNv ? 1.f : shared ? p.sgug[0] : p.gug[uniform(sm.expert[v])];
+        float h[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const uint32_t b = __float_as_uint(acc[q]);
+            const float up = __uint_as_float(__builtin_amdgcn_permlane32_swap(b, b, false, false)[1]);
+            h[q] = gelu_tanh(acc[q] * m) * (up * m);
         }
-    };
-    // the next pass, as many sub-units as fit, and its first requests
-    auto next_pass = [&](int from) {
-        va = from;
-        const int base = pc.rows_before(sm, va), most = P::H_BYTES / pc.pitch;
-        vb = va;
-        for (;;) {   // 64 candidates at a time; the rows only grow
-            const int v = vb + 1 + lane;
-            const int fit = __popcll(__ballot(v <= pc.n && pc.rows_before(sm, min(v, pc.n)) - base <= most));
-            vb += fit;
-            if (fit < 64) break;
+        const int j = ln.g < 2 && t < p.T ? (shared ? 1 : (int)sm.slot[v][t]) : 0;
+        if (j) {
+            uint16_t *base = shared ? p.h_sh : p.h;
+            const size_t row = shared ? (size_t)t : (size_t)t * p.k + j - 1;
+            const uint64_t hv = pack_bf16x2(h[0], h[1]) | (uint64_t)pack_bf16x2(h[2], h[3]) << 32;
+            store_shared(reinterpret_cast<uint64_t *>(MOE_CHECKED(base + row * I + 8 * (u - v * per) + 4 * ln.g, 8, base,
+                                                                  (size_t)p.T * (shared ? 1 : p.k) * I * 2)), hv);
         }
-        vb = uniform(vb);
-        lv = va + wave;
-        lslot = 0;
-        if (lv < vb) {
-            point();
-            for (int i = 0; i < S && lv < vb; ++i) request();
+    }
+};
+
+template <int F, int S, bool XL>
+__device__ __forceinline__ void few_gateup(const FewArgs &p, FewSmem &sm, bool shared, int units, int item) {
+    const FewGateUp<F, S, XL> src(p, sm, shared);
+    FewUnits<F, S, FewGateUp<F, S, XL>> run(src, sm);
+    const int u0 = share_start(item, units, p.n_gu);
+    run.start(u0, share_start(item + 1, units, p.n_gu), u0 / src.per, few_steps(F, p.H));
+    run.run();
+}
+
+// ---------------------------------------------------------------- down
+// The K of the down products comes in segments: an expert's row, or pieces of
+// it where sixteen rows of h would not fit the LDS, then the dense MLP in
+// pieces of the same size.  Units of sixteen output columns of one segment.
+//
+// COLUMNS: an item is one block of columns, all segments, added in registers
+// (out is final).  Otherwise the items share the units evenly, in segment
+// order, so that a workgroup needs few rows of h; each product is stored in
+// fp32 and added by the combine phase.
+//
+// h is staged in LDS for as many segments as fit (a pass); the ring's first
+// weights of a pass are requested before its h is staged, those of the first
+// one before h exists.
+template <int F, int S, bool COLUMNS>
+struct FewDown {
+    static constexpr int KS = FewStep<F>::K;
+    static constexpr int H_BYTES = kFewArea - kFewWaves * S * FewStep<F>::SLOT;   // LDS for rows of h
+    const FewArgs &p;
+    FewSmem &sm;
+    const int ne, PW, pitch;      // segments of an expert, steps of a segment, bytes of one's row of h
+    const int UE, n, blocks;      // segments of the experts, of all; blocks of columns
+    const int r, g;               // this lane's token, its part of a fragment
+    uint8_t *hs;
+    int item = 0, base = 0;       // COLUMNS: the block; rows of h before the pass
+    mutable f32x4 out;            // COLUMNS: sums of this wave's units
+
+    __device__ __forceinline__ FewDown(const FewArgs &p, FewSmem &sm)
+        : p(p), sm(sm), ne(p.ne), PW(p.PW), pitch(p.PW * KS * 2 + 16), UE(uniform(sm.n_experts) * p.ne), n(UE + p.ns),
+          blocks(p.H / 16), r(threadIdx.x & 15), g((threadIdx.x & 63) >> 4), hs(sm.area + kFewWaves * S * FewStep<F>::SLOT) {}
+    __device__ __forceinline__ int at(int u, int v) const {
+        if constexpr (COLUMNS) return u;
+        while (u >= (v + 1) * blocks) ++v;
+        return v;
+    }
+    __device__ __forceinline__ int seg(int u) const { return COLUMNS ? u : u / blocks; }
+    __device__ __forceinline__ int block(int u, int v) const { return COLUMNS ? item : u - v * blocks; }
+    // touched expert of segment v, which of its pieces
+    __device__ __forceinline__ int expert(int v) const { return ne == 1 ? v : v / ne; }
+    __device__ __forceinline__ int piece(int v) const { return v >= UE ? v - UE : ne == 1 ? 0 : v % ne; }
+    // rows of h of the segments before v
+    __device__ __forceinline__ int rows_before(int v) const {
+        if (v >= UE) return p.T * p.k * ne + (v - UE) * p.T;
+        const int e = expert(v), q = v - e * ne, f = sm.first[e];
+        return f * ne + q * (sm.first[e + 1] - f);
+    }
+    __device__ __forceinline__ FewLane<F> lane(int v) const { return FewLane<F>(v >= UE ? p.I_sh : p.I); }
+    __device__ __forceinline__ const uint8_t *weights(int v) const { return v >= UE ? p.swd : p.wd; }
+    __device__ __forceinline__ const uint8_t *scales(int v) const { return v >= UE ? p.sds : p.ds; }
+    __device__ __forceinline__ size_t weight_bytes(int v) const {
+        return (size_t)(v >= UE ? 1 : p.E) * p.H * lane(v).pitch;
+    }
+    __device__ __forceinline__ size_t scale_bytes(int v) const {
+        return (size_t)(v >= UE ? 1 : p.E) * p.H * lane(v).spitch;
+    }
+    __device__ __forceinline__ void span(int v, int &a, int &b) const {
+        a = piece(v) * PW;
+        b = min(few_steps(F, v >= UE ? p.I_sh : p.I), a + PW);
+    }
+    __device__ __forceinline__ FewRows rows(int u, int v) const {
+        const size_t row = (size_t)(v >= UE ? 0 : uniform(sm.expert[expert(v)])) * p.H + 16 * block(u, v);
+        const FewLane<F> ln = lane(v);
+        const uint8_t *w = weights(v) + row * ln.pitch, *s = scales(v) + row * ln.spitch;
+        return ln.rows(w, w + (size_t)8 * ln.pitch, s, s + (size_t)8 * ln.spitch);
+    }
+    // slot of token t in segment v's expert, + 1 (0: not routed there)
+    __device__ __forceinline__ int routed(int v, int t) const { return v >= UE ? t < p.T : (int)sm.slot[expert(v)][t]; }
+    // this lane's row of h: its token's, or, where that is not routed here, the first one (left out by finish)
+    __device__ __forceinline__ const uint8_t *operand(int v) const {
+        const int j = routed(v, r);
+        const int rank = v >= UE ? r : few_count(*reinterpret_cast<const u32x4 *>(sm.slot[expert(v)]), r);
+        return hs + (size_t)(rows_before(v) - base + (j ? rank : 0)) * pitch - 2 * KS * PW * piece(v) +
+               2 * few_frag_k<F>(0, g);
+    }
+    __device__ __forceinline__ u32x4 frag(const uint8_t *x, int st, int i) const {
+        return *reinterpret_cast<const u32x4 *>(x + 2 * KS * st + 2 * few_frag_k<F>(i, 0));
+    }
+    __device__ __forceinline__ void finish(int u, int v, const f32x4 &acc) const {
+        const int t = r, j = routed(v, t);
+        float f = 1.f;
+        if constexpr (F == kFewNv) f = v >= UE ? p.sdg[0] : p.dg[uniform(sm.expert[expert(v)])];
+        if constexpr (COLUMNS) {
+            if (v < UE) f *= sm.w[j ? t * p.k + j - 1 : 0];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) out[q] = j ? fmaf(f, acc[q], out[q]) : out[q];
+        } else if (j) {
+            const int A = p.T * p.k;
+            const size_t row = v >= UE ? (size_t)A * ne + (size_t)(v - UE) * p.T + t : (size_t)A * piece(v) + t * p.k + j - 1;
+            uint64_t *y = reinterpret_cast<uint64_t *>(
+                MOE_CHECKED(p.y + row * p.H + 16 * block(u, v) + 4 * g, 16, p.y, ((size_t)A * ne + p.T * p.ns) * p.H * 4));
+#pragma unroll
+            for (int q = 0; q < 4; q += 2)
+                store_shared(y + q / 2, __float_as_uint(f * acc[q]) | (uint64_t)__float_as_uint(f * acc[q + 1]) << 32);
         }
-    };
+    }
+    // Copies the rows of h of segments va .. vb - 1: segment by segment, its rows in token order.
+    __device__ __forceinline__ void stage(int va, int vb, int wave, int lane) const {
+        for (int v = va + wave; v < vb; v += kFewWaves) {
+            const bool m = v >= UE;
+            const int e = expert(v), f = m ? 0 : uniform(sm.first[e]);
+            const int nr = m ? p.T : uniform(sm.first[e + 1]) - f, I = m ? p.I_sh : p.I;
+            const int a = piece(v) * PW, b = min(few_steps(F, I), a + PW);
+            const int valid = (min(I, b * KS) - a * KS) / 8, all = (b - a) * (KS / 8);   // 16-byte pieces of a row
+            uint8_t *dst = hs + (size_t)(uniform(rows_before(v)) - base) * pitch;
+            for (int i = 0; i < nr; ++i, dst += pitch) {
+                const uint16_t *hb = m ? p.h_sh : p.h;
+                const uint16_t *src = hb + (size_t)(m ? i : uniform(sm.sorted[f + i])) * I + a * KS;
+                for (int c = 0; c < all; c += 64) {
+                    if (c + lane < valid)
+                        dma16<false>(MOE_CHECKED(src + 8 * (c + lane), 16, hb, (size_t)p.T * (m ? 1 : p.k) * I * 2),
+                                     dst + 16 * c);
+                    else if (c + lane < all)   // past the row: the codes there count nothing
+                        *reinterpret_cast<u32x4 *>(dst + 16 * (c + lane)) = u32x4{0u, 0u, 0u, 0u};
+                }
+            }
+        }
+    }
+};
+
+template <int F, int S, bool COLUMNS>
+__device__ __forceinline__ void few_down_items(const FewArgs &p, FewSmem &sm, int item) {
+    using Src = FewDown<F, S, COLUMNS>;
+    const int lane = threadIdx.x & 63, wave = wave_index();
+    Src src(p, sm);
+    FewUnits<F, S, Src> run(src, sm);
     for (bool have_h = false;;) {
-        f32x4 out = {0.f, 0.f, 0.f, 0.f};
+        const int units = COLUMNS ? src.n : src.n * src.blocks;
+        const int u0 = COLUMNS ? 0 : share_start(item, units, p.n_down);
+        const int u1 = COLUMNS ? units : share_start(item + 1, units, p.n_down);
+        src.item = item;
+        src.out = f32x4{0.f, 0.f, 0.f, 0.f};
         int next = 0;
-        for (int from = 0; from < pc.n; from = vb) {
-            // wave 0 polls for h, and loads return in order: its first weights only after that
-            if (wave != 0 || have_h) next_pass(from);
-            if (from == 0) {
+        for (int u = u0; u < u1;) {
+            // the pass: segments va .. vb - 1, as many as fit
+            const int va = src.seg(u), end = src.seg(u1 - 1) + 1, most = Src::H_BYTES / src.pitch;
+            src.base = src.rows_before(va);
+            int vb = va;
+            for (;;) {   // 64 candidates at a time; the rows only grow
+                const int v = vb + 1 + lane;
+                const int fit = __popcll(__ballot(v <= end && src.rows_before(min(v, end)) - src.base <= most));
+                vb += fit;
+                if (fit < 64) break;
+            }
+            vb = uniform(vb);
+            const int ub = COLUMNS ? vb : min(u1, vb * src.blocks);
+            run.start(u, ub, va, src.PW);
+            if (u == u0) {
                 if (threadIdx.x == 0) {
-                    if (!have_h) wait_count(p.ctr + kCtrGateUp, p.n_gu);
-                    sm.down = (int)ctr_add(p.ctr + kCtrDownTicket);
+                    if (!have_h) wait_done(p, kGateUp);
+                    sm.down = (int)ctr_ticket(p, kDown);
                 }
                 __syncthreads();
                 next = uniform(sm.down);
-                if (wave == 0 && !have_h) next_pass(from);
                 have_h = true;
             }
-            // stage the pass's rows of h: sub-unit by sub-unit, its rows in token order
-            const int base = pc.rows_before(sm, va);
-            for (int v = va + wave; v < vb; v += kFewWaves) {
-                const bool mlp = v >= UE;
-                const int e = v / pc.ne, f = mlp ? 0 : uniform(sm.first[e]);
-                const int nr = mlp ? p.T : uniform(sm.first[e + 1]) - f, I = mlp ? p.I_sh : p.I;
-                int a, b;
-                steps(v, a, b);
-                const int valid = (min(I, b * KS) - a * KS) / 8, all = (b - a) * (KS / 8);   // 16-byte pieces of a row
-                uint8_t *dst = hs + (size_t)(uniform(pc.rows_before(sm, v)) - base) * pc.pitch;
-                for (int i = 0; i < nr; ++i, dst += pc.pitch) {
-                    const uint16_t *hb = mlp ? p.h_sh : p.h;
-                    const uint16_t *src = hb + (size_t)(mlp ? i : uniform(sm.sorted[f + i])) * I + a * KS;
-                    for (int c = 0; c < all; c += 64) {
-                        if (c + lane < valid)
-                            dma16<false>(MOE_CHECKED(src + 8 * (c + lane), 16, hb, (size_t)p.T * (mlp ? 1 : p.k) * I * 2),
-                                         dst + 16 * c);
-                        else if (c + lane < all)   // past the row: the codes there count nothing
-                            *reinterpret_cast<u32x4 *>(dst + 16 * (c + lane)) = u32x4{0u, 0u, 0u, 0u};
-                    }
-                }
-            }
+            src.stage(va, vb, wave, lane);
             few_wait<0>();
             __syncthreads();
-            int slot = 0;
-            for (int v = va + wave; v < vb; v += kFewWaves) {
-                const bool mlp = v >= UE;
-                const int e = v / pc.ne;
-                int a, b;
-                steps(v, a, b);
-                // this lane's row: its token's, or, where that is not routed here, the first one (left out below)
-                int j = r < p.T, rank = r;
-                if (!mlp) {
-                    j = sm.slot[e][r];
-                    rank = few_count(*reinterpret_cast<const u32x4 *>(sm.slot[e]), r);
-                }
-                const uint8_t *hr = hs + (size_t)(pc.rows_before(sm, v) - base + (j ? rank : 0)) * pc.pitch;
-                const FewLane<F> ln(mlp ? p.I_sh : p.I);
-                const uint32_t lo = (ln.r & 7) * ln.spitch;
-                f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-                for (int st = a; st < b; ++st) {
-                    const uint8_t *q = ring + slot * SLOT;
-                    if (uniform(lv < vb)) few_wait<(S - 1) * OPS>();
-                    else few_wait<0>();
-                    const uint8_t *hk = hr + 2 * KS * (st - a);
-                    if constexpr (F == kFewBf16) {
+            run.run();
+            u = ub;
+            if (u < u1) __syncthreads();   // the rows of h are free
+        }
+        if constexpr (COLUMNS) {
+            __syncthreads();
+            sm.red[wave][lane] = src.out;
+            __syncthreads();
+            if (threadIdx.x < 256) {
+                const int m = threadIdx.x & 15, t = threadIdx.x >> 4;
+                float sum = 0.f;
 #pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            acc = mfma16x16x32(ln.load(q, i), *reinterpret_cast<const u32x4 *>(hk + 2 * few_frag_k<F>(i, g)),
-                                               acc);
-                    } else {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const u32x4 c = ln.load(q, h);
-                            const uint32_t sc = ln.scale(q, st, h, lo);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                acc = mfma16x16x32(
-                                    few_operand<F>(c, sc, i),
-                                    *reinterpret_cast<const u32x4 *>(hk + 2 * few_frag_k<F>(4 * h + i, g)), acc);
-                        }
-                    }
-                    few_lds_done();
-                    if (uniform(lv < vb)) request();
-                    slot = slot + 1 == S ? 0 : slot + 1;
-                }
-                float f = mlp ? 1.f : sm.w[j ? r * p.k + j - 1 : 0];
-                if constexpr (F == kFewNv) f *= mlp ? p.sdg[0] : p.dg[uniform(sm.expert[e])];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) out[q] = j ? fmaf(f, acc[q], out[q]) : out[q];
+                for (int v = 0; v < kFewWaves; ++v) sum += sm.red[v][16 * (m >> 2) + t][m & 3];
+                if (t < p.T)
+                    *MOE_CHECKED(p.out + (size_t)t * p.H + 16 * item + m, 2, p.out, (size_t)p.T * p.H * 2) =
+                        (uint16_t)f32_to_bf16_rne(sum);
             }
-            if (vb < pc.n) __syncthreads();   // the rows of h are free
+            __syncthreads();   // the sums and the ticket in LDS are free
+        } else {
+            publish(p, kDown, p.n_down);
+            __syncthreads();
         }
-        sm.red[wave][lane] = out;
-        __syncthreads();
-        if (threadIdx.x < 256) {
-            const int m = threadIdx.x & 15, t = threadIdx.x >> 4;
-            float sum = 0.f;
-#pragma unroll
-            for (int v = 0; v < kFewWaves; ++v) sum += sm.red[v][16 * (m >> 2) + t][m & 3];
-            if (t < p.T)
-                *MOE_CHECKED(p.out + (size_t)t * p.H + 16 * item + m, 2, p.out, (size_t)p.T * p.H * 2) =
-                    (uint16_t)f32_to_bf16_rne(sum);
-        }
-        __syncthreads();   // the sums and the ticket in LDS are free
         item = next;
         if ((uint32_t)item >= (uint32_t)p.n_down) return;
     }
-    static_assert(FRAGS * 32 == KS);
+}
+
+// Combine: out[t][c] = sum over token t's slots of w * y, then the dense MLP's
+// segments: in this order, in fp32, rounded once.
+__device__ __forceinline__ void few_combine(const FewArgs &p, const FewSmem &sm, int item) {
+    const int i = item * kFewThreads + threadIdx.x;
+    if (i >= p.T * p.H) return;
+    const int t = i / p.H, c = i - t * p.H, A = p.T * p.k;
+    [[maybe_unused]] const size_t bytes = ((size_t)A * p.ne + p.T * p.ns) * p.H * 4;
+    float sum = 0.f;
+    for (int q = 0; q < p.ne; ++q) {
+        const float *y = p.y + ((size_t)A * q + t * p.k) * p.H + c;
+#pragma unroll 8
+        for (int j = 0; j < p.k; ++j) sum = fmaf(sm.w[t * p.k + j], *MOE_CHECKED(y + (size_t)j * p.H, 4, p.y, bytes), sum);
+    }
+    const float *y = p.y + ((size_t)A * p.ne + t) * p.H + c;
+    for (int q = 0; q < p.ns; ++q) sum += *MOE_CHECKED(y + (size_t)q * p.T * p.H, 4, p.y, bytes);
+    *MOE_CHECKED(p.out + i, 2, p.out, (size_t)p.T * p.H * 2) = (uint16_t)f32_to_bf16_rne(sum);
 }
 
 // S: steps in each wave's ring.  XL: the token rows fit the LDS next to the rings.
 template <int F, int S, bool XL>
 __global__ __launch_bounds__(kFewThreads) void few_layer_kernel(FewArgs p) {
     __shared__ FewSmem sm;
-    if (threadIdx.x == 0) sm.ticket = (int)ctr_add(p.ctr + kCtrRouterTicket);
+    if (threadIdx.x == 0) sm.ticket = (int)ctr_ticket(p, kRouter);
     __syncthreads();
     for (int t = uniform(sm.ticket); (uint32_t)t < (uint32_t)p.n_router;) {
         few_router(p, sm, t);
@@ -599,15 +706,15 @@ __global__ __launch_bounds__(kFewThreads) void few_layer_kernel(FewArgs p) {
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         __syncthreads();
         if (threadIdx.x == 0) {
-            ctr_add(p.ctr + kCtrRouter);
-            sm.ticket = (int)ctr_add(p.ctr + kCtrRouterTicket);
+            ctr_done(p, kRouter, p.n_router);
+            sm.ticket = (int)ctr_ticket(p, kRouter);
         }
         __syncthreads();
         t = uniform(sm.ticket);
     }
     __syncthreads();
     if (threadIdx.x == 0) {
-        const uint32_t a = ctr_add(p.ctr + kCtrGateUpTicket), b = ctr_add(p.ctr + kCtrDownTicket);
+        const uint32_t a = ctr_ticket(p, kGateUp), b = ctr_ticket(p, kDown);
         sm.ticket = (int)a;
         sm.down = (int)b;
     }
@@ -619,43 +726,95 @@ __global__ __launch_bounds__(kFewThreads) void few_layer_kernel(FewArgs p) {
     for (;;) {
         const bool share = (uint32_t)t < (uint32_t)p.n_gu;
         if (share && p.I_sh) {   // needs no routing
-            const int units = p.I_sh / 8;
-            few_gateup<F, S, XL>(p, sm, true, share_start(t, units, p.n_gu), share_start(t + 1, units, p.n_gu));
+            few_gateup<F, S, XL>(p, sm, true, p.I_sh / 8, t);
+            __syncthreads();   // the sums in LDS are free
         }
         if (!selected) few_select(p, sm, t == 0);
         selected = true;
         if (!share) break;
         // the next ticket, early: none is left unless a workgroup has not started yet
-        if (threadIdx.x == 0) sm.ticket = (int)ctr_add(p.ctr + kCtrGateUpTicket);
-        const int units = uniform(sm.n_experts) * (p.I / 8);
-        few_gateup<F, S, XL>(p, sm, false, share_start(t, units, p.n_gu), share_start(t + 1, units, p.n_gu));
-        publish(p.ctr + kCtrGateUp);
+        if (threadIdx.x == 0) sm.ticket = (int)ctr_ticket(p, kGateUp);
+        few_gateup<F, S, XL>(p, sm, false, uniform(sm.n_experts) * (p.I / 8), t);
+        publish(p, kGateUp, p.n_gu);
         t = uniform(sm.ticket);
         __syncthreads();
         if ((uint32_t)t >= (uint32_t)p.n_gu) break;
     }
-    if ((uint32_t)d < (uint32_t)p.n_down) few_down_items<F, S>(p, sm, d);
-    // the last workgroup to leave clears the counters for the next call
-    if (threadIdx.x == 0 && ctr_add(p.ctr + kCtrExit) == gridDim.x - 1) {
-        const int all[6] = {kCtrRouterTicket, kCtrGateUpTicket, kCtrDownTicket, kCtrRouter, kCtrGateUp, kCtrExit};
-        for (int c : all) __hip_atomic_store(p.ctr + c, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if ((uint32_t)d < (uint32_t)p.n_down) {
+        if (p.columns) few_down_items<F, S, true>(p, sm, d);
+        else few_down_items<F, S, false>(p, sm, d);
     }
+    if (!p.columns) {
+        int c = 0;
+        for (bool have_y = false;; have_y = true) {
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                sm.ticket = (int)ctr_ticket(p, kCombine);
+                if (!have_y && (uint32_t)sm.ticket < (uint32_t)p.n_combine) wait_done(p, kDown);
+            }
+            __syncthreads();
+            c = uniform(sm.ticket);
+            if ((uint32_t)c >= (uint32_t)p.n_combine) break;
+            few_combine(p, sm, c);
+        }
+    }
+    // the last workgroup to leave clears the counters for the next call
+    __syncthreads();
+    if (threadIdx.x == 0) sm.ticket = ctr_add(p.ctr + kCtrLine * kCtrExit) == gridDim.x - 1;
+    __syncthreads();
+    if (sm.ticket && threadIdx.x < kCtrWords / kCtrLine)
+        __hip_atomic_store(p.ctr + kCtrLine * threadIdx.x, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// The deepest of three rings that leaves the token rows room; rows that are
-// too long for any are read from global memory.
-template <int F, int S0, int S1, int S2>
-void launch_format(const FewArgs &p, int blocks, hipStream_t st) {
-    const size_t x = (size_t)few_steps(F, p.H) * FewStep<F>::K * 2 * p.T;
-    auto fits = [&](int s) { return x <= (size_t)(kFewArea - kFewWaves * s * FewStep<F>::SLOT); };
-    const dim3 grid(blocks), block(kFewThreads);
-    if (fits(S0)) few_layer_kernel<F, S0, true><<<grid, block, 0, st>>>(p);
-    else if (fits(S1)) few_layer_kernel<F, S1, true><<<grid, block, 0, st>>>(p);
-    else if (fits(S2)) few_layer_kernel<F, S2, true><<<grid, block, 0, st>>>(p);
-    else few_layer_kernel<F, S1, false><<<grid, block, 0, st>>>(p);
+// Steps in a ring: the deepest that leaves the token rows room (bf16 or 4-bit,
+// by slot size); the last with rows that are too long for any, read from
+// global memory.
+constexpr int kRings = 4, kRing[2][kRings + 1] = {{7, 5, 4, 3, 5}, {6, 5, 4, 2, 5}};
+
+struct FewPlan {
+    int ring;      // of kRing
+    bool columns;
+    int PW, ne, ns;
+    size_t y;      // floats of the products' workspace
+};
+
+int few_slot(int f) { return f == kFewBf16 ? FewStep<kFewBf16>::SLOT : FewStep<kFewMx>::SLOT; }
+static_assert(FewStep<kFewMx>::SLOT == FewStep<kFewNv>::SLOT, "one ring for both");
+
+FewPlan few_plan(int f, int T, int H, int k, int I, int I_sh) {
+    FewPlan g{};
+    const int *rings = kRing[f != kFewBf16], step = f == kFewBf16 ? FewStep<kFewBf16>::K * 2 : FewStep<kFewMx>::K * 2;
+    auto rest = [&](int i) { return kFewArea - kFewWaves * rings[i] * few_slot(f); };
+    while (g.ring < kRings && (long long)few_steps(f, H) * step * T > rest(g.ring)) ++g.ring;
+    // segments of which T rows of h fit
+    const int most = (rest(g.ring) / T - 16) / step, st = few_steps(f, I), want = (st + most - 1) / most;
+    g.PW = (st + want - 1) / want;
+    g.ne = (st + g.PW - 1) / g.PW;
+    g.ns = (few_steps(f, I_sh) + g.PW - 1) / g.PW;
+    g.columns = T * k <= 16;
+    g.y = g.columns ? 0 : ((size_t)T * k * g.ne + (size_t)T * g.ns) * H;
+    return g;
 }
+
+template <int F, int R = 0>
+void launch_format(const FewArgs &p, int ring, int blocks, hipStream_t st) {
+    constexpr int S = kRing[F != kFewBf16][R];
+    static_assert((kFewArea - kFewWaves * S * FewStep<F>::SLOT) / kFewTokens >= 16 + FewStep<F>::K * 2,
+                  "a segment is one step or more");
+    if (ring == R) {
+        few_layer_kernel<F, S, R != kRings><<<blocks, kFewThreads, 0, st>>>(p);
+        return;
+    }
+    if constexpr (R < kRings) launch_format<F, R + 1>(p, ring, blocks, st);
+}
+
+int few_format(WeightFormat f) { return f == WeightFormat::kBF16 ? kFewBf16 : f == WeightFormat::kMXFP4 ? kFewMx : kFewNv; }
 
 }  // namespace
+
+size_t few_layer_y(WeightFormat fmt, int T, int H, int k, int I, int I_sh) {
+    return few_plan(few_format(fmt), T, H, k, I, I_sh).y * sizeof(float);
+}
 
 hipError_t launch_few_layer(const FewLayer &l, hipStream_t st) {
     FewArgs p{};
@@ -681,6 +840,7 @@ hipError_t launch_few_layer(const FewLayer &l, hipStream_t st) {
     p.logits = l.logits;
     p.h = l.h;
     p.h_sh = l.h_sh;
+    p.y = l.y;
     p.T = l.T;
     p.H = l.H;
     p.E = l.E;
@@ -692,12 +852,20 @@ hipError_t launch_few_layer(const FewLayer &l, hipStream_t st) {
     const long long units = (long long)std::min(l.E, l.T * l.k) * (l.I / 8);   // at most
     p.n_router = (l.E + 3) / 4;
     p.n_gu = (int)std::min<long long>(kBlocks, std::max<long long>(units, l.I_sh / 8));
-    p.n_down = l.H / 16;
+    const int f = few_format(l.fmt);
+    const FewPlan g = few_plan(f, l.T, l.H, l.k, l.I, l.I_sh);
+    p.columns = g.columns;
+    p.PW = g.PW;
+    p.ne = g.ne;
+    p.ns = g.ns;
+    // (no item is empty: k experts at least are touched)
+    p.n_down = g.columns ? l.H / 16 : std::min(kBlocks, (l.k * g.ne + g.ns) * (l.H / 16));
+    p.n_combine = (l.T * l.H + kFewThreads - 1) / kFewThreads;
     const int blocks = std::min(kBlocks, std::max(p.n_router, std::max(p.n_gu, p.n_down)));
-    switch (l.fmt) {
-        case WeightFormat::kBF16: launch_format<kFewBf16, 7, 5, 3>(p, blocks, st); break;
-        case WeightFormat::kMXFP4: launch_format<kFewMx, 5, 4, 2>(p, blocks, st); break;
-        default: launch_format<kFewNv, 5, 4, 2>(p, blocks, st);
+    switch (f) {
+        case kFewBf16: launch_format<kFewBf16>(p, g.ring, blocks, st); break;
+        case kFewMx: launch_format<kFewMx>(p, g.ring, blocks, st); break;
+        default: launch_format<kFewNv>(p, g.ring, blocks, st);
     }
     return hipGetLastError();
 }

@@ -33,15 +33,19 @@ constexpr int kFewTokens = 16;   // MFMA columns
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 __device__ __forceinline__ int wave_index() { return uniform(threadIdx.x >> 6); }
 
-template <int F>
+// ODD: scale rows of NVFP4 may start in the middle of a word (K a multiple of
+// 32 but not of 64).
+template <int F, bool ODD = false>
 struct FewStep {
     static constexpr int K = F == kFewBf16 ? 64 : 256;           // K values
     static constexpr int FRAGS = K / 32;                          // MFMAs
-    // ring slot: 16 rows of 128 bytes, then (MXFP4, NVFP4) the lanes' scale words of the two pieces
-    static constexpr bool SCALES = F == kFewMx || F == kFewNv;
-    static constexpr int SLOT = 2048 + (SCALES ? 512 : 0);
-    static constexpr int OPS = 2 + (SCALES ? 2 : 0);              // loads
-    static constexpr int SB = F == kFewNv ? 2 : 1;                // scale bytes of a piece
+    static constexpr int SB = F == kFewMx ? 1 : F == kFewNv ? 2 : 0;   // scale bytes of a piece (8 pieces)
+    // Scales (MXFP4, NVFP4): the aligned words that hold a row's 8 or 16 bytes, four to a load of the wave (one
+    // load a step rather than each lane its own words: those are half the requests of a step, and take the
+    // time of as many cache lines).
+    static constexpr int SOPS = SB == 0 ? 0 : ODD && F == kFewNv ? 2 : 1;
+    static constexpr int SLOT = 2048 + 256 * SOPS;                // ring slot: 16 rows of 128 bytes, the scale words
+    static constexpr int OPS = 2 + SOPS;                          // loads
     // Whole lines read once carry the non-temporal hint; 4-bit rows of a multiple of 32 bytes straddle lines,
     // whose other part the next step wants.
     static constexpr bool STREAM = F == kFewBf16;
@@ -63,23 +67,23 @@ __device__ __forceinline__ u32x4 few_i4_order(const u32x4 &v) {
                  (v[1] & 0xFFFFu) | (v[3] << 16), (v[1] >> 16) | (v[3] & 0xFFFF0000u)};
 }
 
-// Addresses of a matrix's steps for one lane.  Sixteen rows are two blocks of
-// eight consecutive rows (`top` and `low`); lane l loads 16 bytes of row l / 8
-// of each, the piece swizzled so that the fragment reads have no bank
-// conflicts.  A 4-bit row may end inside a step: pieces past its end read the
-// row's first piece, whose codes then meet zero token values.
-template <int F>
+// Where one lane loads the steps of sixteen rows from: 16 bytes of row l / 8
+// of each of two blocks of eight consecutive rows, the piece swizzled so that
+// the fragment reads have no bank conflicts, and a scale word.  A 4-bit row
+// may end inside a step: pieces past its end read the row's last piece, whose
+// codes then meet zero token values.
 struct FewRows {
-    const uint8_t *top, *low;      // weight rows
-    const uint8_t *stop, *slow;    // scale rows
-    int ntop = 7, nlow = 7;        // last row of each block that exists (the others repeat it)
+    const uint8_t *top, *low;   // of step 0
+    const uint8_t *scale;
+    uint32_t last_scale;        // offset of the last scale word of the row
 };
 
-template <int F>
+template <int F, bool ODD = false>
 struct FewLane {
+    using Step = FewStep<F, ODD>;
     int pieces;                    // of a row
     uint32_t pitch, spitch;        // bytes of a row of weights, of scales
-    uint32_t row, piece;           // loads: this lane's row of a block, its piece within a step
+    uint32_t piece;                // loads: this lane's piece within a step
     uint32_t r, g;
 
     __device__ __forceinline__ explicit FewLane(int k) {
@@ -87,47 +91,49 @@ struct FewLane {
         pitch = F == kFewBf16 ? 2 * k : k / 2;
         spitch = F == kFewMx ? k / 32 : k / 16;
         pieces = k / (F == kFewBf16 ? 8 : 32);
-        row = l >> 3;
-        piece = (l & 7) ^ row;
+        piece = (l & 7) ^ (l >> 3);
         r = l & 15;
         g = l >> 4;
     }
-    // offset in its scale row of the scales of piece 4 h + g of step s; the row's first past its end
-    __device__ __forceinline__ uint32_t scale_at(int s, int h) const {
-        const int p = 8 * s + 4 * h + (int)g;
-        return FewStep<F>::SB * (p < pieces ? p : 0);
-    }
-    // scale row of MFMA row r
-    __device__ __forceinline__ const uint8_t *scale_row(const FewRows<F> &m) const {
-        return r < 8 ? m.stop + min((int)r, m.ntop) * (size_t)spitch : m.slow + min((int)r - 8, m.nlow) * (size_t)spitch;
+    // Rows from `top` and `low` on (scales from `stop` and `slow` on); ntop, nlow: the last of each block's
+    // eight rows that exists (the others repeat it).
+    __device__ __forceinline__ FewRows rows(const uint8_t *top, const uint8_t *low, const uint8_t *stop,
+                                            const uint8_t *slow, int ntop = 7, int nlow = 7) const {
+        const int l = threadIdx.x & 63, row = l >> 3, q = l >> 2;
+        FewRows m{top + min(row, ntop) * (size_t)pitch, low + min(row, nlow) * (size_t)pitch, nullptr, 0};
+        if constexpr (Step::SOPS > 0) {
+            const uintptr_t at = reinterpret_cast<uintptr_t>(q < 8 ? stop + min(q, ntop) * (size_t)spitch
+                                                                   : slow + min(q - 8, nlow) * (size_t)spitch);
+            m.scale = reinterpret_cast<const uint8_t *>(at & ~(uintptr_t)3);
+            m.last_scale = (((uint32_t)at & 3) + spitch - 1) & ~3u;
+        }
+        return m;
     }
     // Requests step s into `slot` (wave-uniform).  wb, wn / sb, sn: the extent of the matrices (debug build).
-    __device__ __forceinline__ void issue(const FewRows<F> &m, int s, uint8_t *slot, [[maybe_unused]] const void *wb,
+    __device__ __forceinline__ void issue(const FewRows &m, int s, uint8_t *slot, [[maybe_unused]] const void *wb,
                                           [[maybe_unused]] size_t wn, [[maybe_unused]] const void *sb,
                                           [[maybe_unused]] size_t sn) const {
-        const uint32_t off = F != kFewBf16 && 8 * s + (int)piece >= pieces ? 0u : 128 * s + 16 * piece;
-        dma16<FewStep<F>::STREAM>(MOE_CHECKED(m.top + (min((int)row, m.ntop) * (size_t)pitch + off), 16, wb, wn), slot);
-        dma16<FewStep<F>::STREAM>(MOE_CHECKED(m.low + (min((int)row, m.nlow) * (size_t)pitch + off), 16, wb, wn),
-                                  slot + 1024);
-        if constexpr (FewStep<F>::SCALES) {
-            // the aligned word that holds this lane's one or two scale bytes
-            const uint8_t *base = scale_row(m);
+        uint32_t off = 128 * s + 16 * piece;
+        if constexpr (F != kFewBf16) off = min(off, 16u * pieces - 16);
+        dma16<Step::STREAM>(MOE_CHECKED(m.top + off, 16, wb, wn), slot);
+        dma16<Step::STREAM>(MOE_CHECKED(m.low + off, 16, wb, wn), slot + 1024);
+        // words l % 4 (and 4 + l % 4) of row l / 4, none past the one that ends the row
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uintptr_t at = reinterpret_cast<uintptr_t>(base + scale_at(s, h));
-                dma4(MOE_CHECKED(reinterpret_cast<const uint8_t *>(at & ~(uintptr_t)3), 4, sb, (sn + 3) & ~(size_t)3),
-                     slot + 2048 + 256 * h);
-            }
-        }
+        for (int h = 0; h < Step::SOPS; ++h)
+            dma4(MOE_CHECKED(m.scale + min(8 * Step::SB * s + 16 * h + 4 * (threadIdx.x & 3), m.last_scale), 4, sb,
+                             (sn + 3) & ~(size_t)3),
+                 slot + 2048 + 256 * h);
     }
     // 16-byte piece 4 h + g of this lane's row in a slot whose loads are complete
     __device__ __forceinline__ u32x4 load(const uint8_t *slot, int h) const {
         return *reinterpret_cast<const u32x4 *>(slot + 128 * r + (((4 * h + g) ^ (r & 7)) << 4));
     }
-    // its scales; lo: the address of its scale row modulo 4
+    // its scales (0 past the row's end); lo: the address of its scale row modulo 4
     __device__ __forceinline__ uint32_t scale(const uint8_t *slot, int s, int h, uint32_t lo) const {
-        const uint32_t w = *reinterpret_cast<const uint32_t *>(slot + 2048 + 256 * h + 4 * (threadIdx.x & 63));
-        return (w >> (8 * ((lo + scale_at(s, h)) & 3))) & (F == kFewMx ? 0xFFu : 0xFFFFu);
+        const uint32_t p = 4 * h + g, at = (lo & 3) + Step::SB * p;
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(slot + 2048 + 16 * (at & ~15u) + 16 * r + (at & 12));
+        const uint32_t v = (w >> (8 * (at & 3))) & (F == kFewMx ? 0xFFu : 0xFFFFu);
+        return (int)(8 * s + p) < pieces ? v : 0u;
     }
 };
 

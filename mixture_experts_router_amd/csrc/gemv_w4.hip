@@ -55,8 +55,8 @@ static_assert(sizeof(GemvSmem) <= 160 * 1024, "LDS of one workgroup");
 template <int F, int GROUP, bool ZEROS>
 struct GemvSlot {
     static constexpr int NS = F == kFewI4 ? (GROUP == 32 ? 2 : 1) : 0;
-    static constexpr int SLOT = FewStep<F>::SLOT + 256 * NS * (ZEROS ? 2 : 1);
-    static constexpr int OPS = FewStep<F>::OPS + NS * (ZEROS ? 2 : 1);
+    static constexpr int SLOT = FewStep<F, true>::SLOT + 256 * NS * (ZEROS ? 2 : 1);
+    static constexpr int OPS = FewStep<F, true>::OPS + NS * (ZEROS ? 2 : 1);
 };
 
 // Weight row of the MFMA's row m in unit u, clamped to a row that exists (the
@@ -105,7 +105,7 @@ __global__ __launch_bounds__(kGemvThreads) void gemv_w4_kernel(GemvArgs p) {
     const int T = p.T, K = p.K, tr = min(r, T - 1);
     const int KW = few_kwaves(u1 - u0, c1 - c0), UG = kGemvWaves / KW, kw = wave % KW;
     const int s0 = c0 + kw * (c1 - c0) / KW, s1 = c0 + (kw + 1) * (c1 - c0) / KW;
-    const FewLane<F> ln(K);
+    const FewLane<F, true> ln(K);   // NVFP4 rows of 32 K values more or less
     uint8_t *ring = sm.area + wave * S * SLOT, *xs = sm.area + kGemvWaves * S * SLOT;
     const int nx = (c1 - c0) * FRAGS * 4 * T;   // 16-byte pieces of the token rows
     [[maybe_unused]] float *xsum = reinterpret_cast<float *>(xs + (size_t)nx * 16);
@@ -116,16 +116,13 @@ __global__ __launch_bounds__(kGemvThreads) void gemv_w4_kernel(GemvArgs p) {
 
     // the step to request next: of unit lu
     int lu = u0 + wave / KW, ls = s0, lslot = 0;
-    FewRows<F> rows;
+    FewRows rows;
     [[maybe_unused]] size_t lgroup = 0;         // INT4: first group of this lane's row (MFMA row lane % 16)
     auto point = [&]() {
         const int top = p.geglu ? 8 * lu : 16 * lu, low = p.geglu ? p.outs + top : min(top + 8, p.N - 1);
-        rows.ntop = min(7, (p.geglu ? p.outs : p.N) - 1 - top);
-        rows.nlow = p.geglu ? rows.ntop : min(7, p.N - 1 - low);
-        rows.top = p.w + (size_t)top * ln.pitch;
-        rows.low = p.w + (size_t)low * ln.pitch;
-        rows.stop = p.scales + (size_t)top * ln.spitch;
-        rows.slow = p.scales + (size_t)low * ln.spitch;
+        const int ntop = min(7, (p.geglu ? p.outs : p.N) - 1 - top), nlow = p.geglu ? ntop : min(7, p.N - 1 - low);
+        rows = ln.rows(p.w + (size_t)top * ln.pitch, p.w + (size_t)low * ln.pitch, p.scales + (size_t)top * ln.spitch,
+                       p.scales + (size_t)low * ln.spitch, ntop, nlow);
         if constexpr (F == kFewI4) lgroup = (size_t)gemv_row(p, lu, r) * pg;
     };
     auto request = [&]() {
@@ -182,6 +179,7 @@ __global__ __launch_bounds__(kGemvThreads) void gemv_w4_kernel(GemvArgs p) {
     int slot = 0;
     for (int v0 = u0; v0 < u1; v0 += UG) {
         f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+        [[maybe_unused]] f32x4 half[2] = {acc, acc};   // of the two halves of every step
         const int u = v0 + wave / KW;
         if (uniform(u < u1)) {
             // where in its word a scale (zero) of this lane's rows lies: the low bits of its index
@@ -194,7 +192,7 @@ __global__ __launch_bounds__(kGemvThreads) void gemv_w4_kernel(GemvArgs p) {
             }
             for (int st = s0; st < s1; ++st) {
                 const uint8_t *q = ring + slot * SLOT;
-                if (uniform(lu < u1)) few_wait<(S - 1) * OPS>();
+                if (lu < u1) few_wait<(S - 1) * OPS>();
                 else few_wait<0>();
                 const uint8_t *xq = xl + (size_t)(st - c0) * FRAGS * 64 * T;
                 if constexpr (F == kFewI4) {
@@ -226,22 +224,27 @@ __global__ __launch_bounds__(kGemvThreads) void gemv_w4_kernel(GemvArgs p) {
                             part = f32x4{0.f, 0.f, 0.f, 0.f};
                         }
                     }
+                    few_lds_done();
+                    if (lu < u1) request();
                 } else {
+                    // everything of the step into registers at once, then its slot is free for another
+                    const u32x4 c[2] = {ln.load(q, 0), ln.load(q, 1)};
+                    const uint32_t sc[2] = {ln.scale(q, st, 0, lo), ln.scale(q, st, 1, lo)};
+                    u32x4 xf[FRAGS];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const u32x4 c = ln.load(q, h);
-                        const uint32_t sc = ln.scale(q, st, h, lo);
+                    for (int f = 0; f < FRAGS; ++f) xf[f] = *reinterpret_cast<const u32x4 *>(xq + f * 64 * T);
+                    few_lds_done();
+                    if (lu < u1) request();
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            acc = mfma16x16x32(few_operand<F>(c, sc, i),
-                                               *reinterpret_cast<const u32x4 *>(xq + (4 * h + i) * 64 * T), acc);
-                    }
+                            half[h] = mfma16x16x32(few_operand<F>(c[h], sc[h], i), xf[4 * h + i], half[h]);
                 }
-                few_lds_done();
-                if (uniform(lu < u1)) request();
                 slot = slot + 1 == S ? 0 : slot + 1;
             }
         }
+        if constexpr (F != kFewI4) acc = half[0] + half[1];
         sm.red[wave][lane] = acc;
         __syncthreads();
         // four waves finish a unit (lane 16 (m / 4) + t, element m % 4 of each wave's sums: weight row m, token t)
@@ -312,7 +315,7 @@ GemvPlan gemv_plan(GemvFormat fmt, int group, bool zeros, int T, int N, int K, b
     g.outs = geglu ? N / 2 : N;
     g.units = geglu ? (g.outs + 7) / 8 : (N - 1) / 16 + 1;
     const int steps = (K - 1) / 256 + 1;
-    const int words = fmt == GemvFormat::kINT4 ? (group == 32 ? 2 : 1) * (zeros ? 2 : 1) : 2;
+    const int words = fmt == GemvFormat::kINT4 ? (group == 32 ? 2 : 1) * (zeros ? 2 : 1) : fmt == GemvFormat::kNVFP4 ? 2 : 1;
     const int fit = (int)((kGemvArea - gemv_ring_bytes(2048 + 256 * words, kGemvShallow)) / gemv_x_bytes(T, 1));
     g.slices = (steps + fit - 1) / fit;
     g.ranges = std::min(g.units, std::max(1, kGemvBlocks / g.slices));

@@ -122,9 +122,11 @@ struct FewLayer {
     uint32_t *counters;      // kFewCounterBytes, zero before the launch and after it
     float *logits;           // [T][E]
     uint16_t *h, *h_sh;      // [T*k][I], [T][I_sh]
+    float *y;                // few_layer_y bytes: the down products before they are added
     int T, H, E, k, I, I_sh;
 };
-constexpr int kFewCounterBytes = 1024;
+constexpr int kFewCounterBytes = 4096;
+size_t few_layer_y(WeightFormat fmt, int T, int H, int k, int I, int I_sh);
 hipError_t launch_few_layer(const FewLayer &l, hipStream_t st);
 
 // Matrix-vector products with 4-bit weights for up to kFewMaxT tokens.
