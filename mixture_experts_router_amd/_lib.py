@@ -164,9 +164,10 @@ def _ptr(t):
 
 
 def _stream(stream):
-    import torch
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the current device's current stream, without building a Stream object: a third of a small call's host time
+        from torch import _C
+        return _C._cuda_getCurrentRawStream(_C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 

@@ -283,141 +283,38 @@ __device__ void few_stage_x(const FewArgs &p, uint8_t *xs) {
     __syncthreads();
 }
 
-// A workgroup's run of units, each an MFMA tile of sixteen weight rows summed
-// along its steps.  Whole rounds of eight units go a unit to a wave and need no
-// barrier; the units that are left (fewer than eight) are split along K so that
-// no wave is longer at work than it must, and their sums joined.  The order of
-// each unit's sum depends on the run alone.
-//
-// Src says what the units are: at(u, v) (its segment of the weights, v or a
-// later one), lane(v) (the row length), span(v, a, b) (its steps), rows(u, v),
-// operand(v) (this lane's token data), frag(operand, step, i), finish(u, v,
-// sums).
-template <int F, int S, class Src>
-struct FewUnits {
-    static constexpr int SLOT = FewStep<F>::SLOT, OPS = FewStep<F>::OPS, FRAGS = FewStep<F>::FRAGS;
-    const Src &src;
-    FewSmem &sm;
-    uint8_t *ring;
-    int wave, lane;
-    int u0 = 0, um = 0, u1 = 0, KW = 1, UG = 1;      // the run; um: the units that are left, UG at a time
-    int v0 = 0;                                       // its first segment
-    int lu = 0, lv = 0, ls = 0, ls1 = 0, lslot = 0;   // the step to request next (u1: none) and its slot
-    FewRows rows;
-
-    __device__ __forceinline__ FewUnits(const Src &src, FewSmem &sm)
-        : src(src), sm(sm), wave(wave_index()), lane(threadIdx.x & 63) {
-        ring = sm.area + wave * S * SLOT;
-    }
-    // this wave's steps of unit u of segment v
-    __device__ __forceinline__ void part(int u, int v, int &a, int &b) const {
-        src.span(v, a, b);
-        if (u >= um) {
-            const int kw = wave & (KW - 1), n = b - a;
-            b = a + (kw + 1) * n / KW;
-            a += kw * n / KW;
-        }
-    }
-    // the next unit with steps for this wave: u, or one after it (left: u is one of the units that are left)
-    __device__ __forceinline__ void seek(int u, bool left) {
-        for (;; u += left ? UG : kFewWaves) {
-            if (!left && u >= um) {
-                left = true;
-                u = um + wave / KW;
-            }
-            lu = u1;
-            if (u >= u1) return;
-            lv = src.at(u, lv);
-            part(u, lv, ls, ls1);
-            if (ls < ls1) break;   // not where there are more waves than steps
-        }
-        lu = u;
-        rows = src.rows(u, lv);
-    }
-    __device__ __forceinline__ void request() {
-        src.lane(lv).issue(rows, ls, ring + lslot * SLOT, src.weights(lv), src.weight_bytes(lv), src.scales(lv),
-                           src.scale_bytes(lv));
-        lslot = lslot + 1 == S ? 0 : lslot + 1;
-        if (++ls == ls1) seek(lu + (lu >= um ? UG : kFewWaves), lu >= um);
-    }
-    // Requests the first steps of units a .. b - 1, a of segment v, each of at most `steps` steps.
-    __device__ __forceinline__ void start(int a, int b, int v, int steps) {
-        u0 = a;
-        u1 = b;
-        um = b - (b - a) % kFewWaves;
-        KW = few_kwaves(b - um, steps);
-        UG = kFewWaves / KW;
-        v0 = lv = v;
-        lslot = 0;
-        seek(u0 + wave, false);
-        for (int i = 0; i < S && lu < u1; ++i) request();
-    }
-    __device__ __forceinline__ void run() {
-        int slot = 0, v = v0;
-        for (int i = u0; i < u1;) {
-            const bool left = i >= um;
-            const int u = i + (left ? wave / KW : wave);
-            f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-            if (uniform(u < u1)) {
-                v = src.at(u, v);
-                const auto ln = src.lane(v);
-                const auto x = src.operand(v);
-                // (a unit's scale rows start at a multiple of 4 bytes)
-                [[maybe_unused]] const uint32_t lo = (ln.r & 7) * ln.spitch;
-                int a, b;
-                part(u, v, a, b);
-                for (int st = a; st < b; ++st) {
-                    const uint8_t *q = ring + slot * SLOT;
-                    // the ring is full but for this step's successors: S - 1 steps may be in flight
-                    if (lu < u1) few_wait<(S - 1) * OPS>();
-                    else few_wait<0>();
-                    // everything of the step into registers at once, then its slot is free for another
-                    const u32x4 c[2] = {ln.load(q, 0), ln.load(q, 1)};
-                    [[maybe_unused]] uint32_t sc[2];
-                    if constexpr (FewStep<F>::SOPS > 0) {
-                        sc[0] = ln.scale(q, st, 0, lo);
-                        sc[1] = ln.scale(q, st, 1, lo);
-                    }
-                    u32x4 xf[FRAGS];
-#pragma unroll
-                    for (int f = 0; f < FRAGS; ++f) xf[f] = src.frag(x, st, f);
-                    few_lds_done();
-                    if (lu < u1) request();
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if constexpr (F == kFewBf16) {
-                            acc[h] = mfma16x16x32(c[h], xf[h], acc[h]);
-                        } else {
-#pragma unroll
-                            for (int f = 0; f < 4; ++f)
-                                acc[h] = mfma16x16x32(few_operand<F>(c[h], sc[h], f), xf[4 * h + f], acc[h]);
-                        }
-                    }
-                    slot = slot + 1 == S ? 0 : slot + 1;
-                }
-            }
-            const f32x4 sum = acc[0] + acc[1];
-            if (!left) {
-                src.finish(u, v, sum);
-            } else {
-                sm.red[wave][lane] = sum;
-                __syncthreads();
-                if (uniform(wave < UG && i + wave < u1)) {
-                    f32x4 all = {0.f, 0.f, 0.f, 0.f};
-                    for (int w = 0; w < KW; ++w) all += sm.red[wave * KW + w][lane];
-                    src.finish(i + wave, src.at(i + wave, v0), all);
-                }
-                __syncthreads();
-            }
-            i += left ? UG : kFewWaves;
-        }
-    }
+// A lane's token data of a unit, its row of weights, and the address of that
+// row's scales modulo 4 (a unit's first scale row starts at a multiple of 4).
+template <int F>
+struct FewOperand {
+    const uint8_t *x;
+    FewLane<F> ln;
+    uint32_t lo;
+    __device__ __forceinline__ FewOperand(const uint8_t *x, const FewLane<F> &ln)
+        : x(x), ln(ln), lo((ln.r & 7) * ln.spitch) {}
 };
+
+// A step out of its slot and the token rows of Src.
+template <int F, class Src>
+__device__ __forceinline__ FewData<F> few_fetch(const Src &src, const uint8_t *q, int st, const FewOperand<F> &o) {
+    FewData<F> d;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        d.c[h] = o.ln.load(q, h);
+        d.sc[h] = 0;
+        if constexpr (FewStep<F>::SOPS > 0) d.sc[h] = o.ln.scale(q, st, h, o.lo);
+    }
+#pragma unroll
+    for (int f = 0; f < FewStep<F>::FRAGS; ++f) d.x[f] = src.frag(o.x, st, f);
+    return d;
+}
 
 // Gate/up units of eight h columns: the MFMA's rows are the unit's eight gate
 // rows and the matching eight up rows.
-template <int F, int S, bool XL>
+template <int F, int S_, bool XL>
 struct FewGateUp {
+    static constexpr int S = S_, SLOT = FewStep<F>::SLOT, OPS = FewStep<F>::OPS;
+    using Rows = FewRows;
     const FewArgs &p;
     FewSmem &sm;
     const bool shared;
@@ -444,11 +341,20 @@ struct FewGateUp {
         const uint8_t *w = weights(v) + row * ln.pitch, *s = scales(v) + row * ln.spitch;
         return ln.rows(w, w + (size_t)I * ln.pitch, s, s + (size_t)I * ln.spitch);
     }
+    __device__ __forceinline__ void issue(const FewRows &m, int v, int st, uint8_t *slot) const {
+        lane(v).issue(m, st, slot, weights(v), weight_bytes(v), scales(v), scale_bytes(v));
+    }
+    __device__ __forceinline__ FewData<F> fetch(const uint8_t *q, int st, const FewOperand<F> &o) const {
+        return few_fetch<F>(*this, q, st, o);
+    }
+    __device__ __forceinline__ void multiply(const FewData<F> &d, int, const FewOperand<F> &, f32x4 (&acc)[2]) const {
+        few_multiply<F>(d, acc);
+    }
     // XL: the token rows are in LDS, every fragment as 16 bytes per (g, token)
-    __device__ __forceinline__ const uint8_t *operand(int) const {
+    __device__ __forceinline__ FewOperand<F> operand(int, int) const {
         const int t = min((int)ln.r, p.T - 1);
-        if constexpr (XL) return sm.area + kFewWaves * S * FewStep<F>::SLOT + (ln.g * p.T + t) * 16;
-        return reinterpret_cast<const uint8_t *>(p.x + (size_t)t * p.H);
+        if constexpr (XL) return {sm.area + kFewWaves * S * SLOT + (ln.g * p.T + t) * 16, ln};
+        return {reinterpret_cast<const uint8_t *>(p.x + (size_t)t * p.H), ln};
     }
     __device__ __forceinline__ u32x4 frag(const uint8_t *x, int st, int i) const {
         const int f = st * FewStep<F>::FRAGS + i;
@@ -484,7 +390,7 @@ struct FewGateUp {
 template <int F, int S, bool XL>
 __device__ __forceinline__ void few_gateup(const FewArgs &p, FewSmem &sm, bool shared, int units, int item) {
     const FewGateUp<F, S, XL> src(p, sm, shared);
-    FewUnits<F, S, FewGateUp<F, S, XL>> run(src, sm);
+    FewUnits<FewGateUp<F, S, XL>> run(src, sm.area, sm.red);
     const int u0 = share_start(item, units, p.n_gu);
     run.start(u0, share_start(item + 1, units, p.n_gu), u0 / src.per, few_steps(F, p.H));
     run.run();
@@ -503,10 +409,12 @@ __device__ __forceinline__ void few_gateup(const FewArgs &p, FewSmem &sm, bool s
 // h is staged in LDS for as many segments as fit (a pass); the ring's first
 // weights of a pass are requested before its h is staged, those of the first
 // one before h exists.
-template <int F, int S, bool COLUMNS>
+template <int F, int S_, bool COLUMNS>
 struct FewDown {
+    static constexpr int S = S_, SLOT = FewStep<F>::SLOT, OPS = FewStep<F>::OPS;
+    using Rows = FewRows;
     static constexpr int KS = FewStep<F>::K;
-    static constexpr int H_BYTES = kFewArea - kFewWaves * S * FewStep<F>::SLOT;   // LDS for rows of h
+    static constexpr int H_BYTES = kFewArea - kFewWaves * S * SLOT;   // LDS for rows of h
     const FewArgs &p;
     FewSmem &sm;
     const int ne, PW, pitch;      // segments of an expert, steps of a segment, bytes of one's row of h
@@ -556,12 +464,21 @@ struct FewDown {
     }
     // slot of token t in segment v's expert, + 1 (0: not routed there)
     __device__ __forceinline__ int routed(int v, int t) const { return v >= UE ? t < p.T : (int)sm.slot[expert(v)][t]; }
+    __device__ __forceinline__ void issue(const FewRows &m, int v, int st, uint8_t *slot) const {
+        lane(v).issue(m, st, slot, weights(v), weight_bytes(v), scales(v), scale_bytes(v));
+    }
+    __device__ __forceinline__ FewData<F> fetch(const uint8_t *q, int st, const FewOperand<F> &o) const {
+        return few_fetch<F>(*this, q, st, o);
+    }
+    __device__ __forceinline__ void multiply(const FewData<F> &d, int, const FewOperand<F> &, f32x4 (&acc)[2]) const {
+        few_multiply<F>(d, acc);
+    }
     // this lane's row of h: its token's, or, where that is not routed here, the first one (left out by finish)
-    __device__ __forceinline__ const uint8_t *operand(int v) const {
+    __device__ __forceinline__ FewOperand<F> operand(int, int v) const {
         const int j = routed(v, r);
         const int rank = v >= UE ? r : few_count(*reinterpret_cast<const u32x4 *>(sm.slot[expert(v)]), r);
-        return hs + (size_t)(rows_before(v) - base + (j ? rank : 0)) * pitch - 2 * KS * PW * piece(v) +
-               2 * few_frag_k<F>(0, g);
+        return {hs + (size_t)(rows_before(v) - base + (j ? rank : 0)) * pitch - 2 * KS * PW * piece(v) +
+                    2 * few_frag_k<F>(0, g), lane(v)};
     }
     __device__ __forceinline__ u32x4 frag(const uint8_t *x, int st, int i) const {
         return *reinterpret_cast<const u32x4 *>(x + 2 * KS * st + 2 * few_frag_k<F>(i, 0));
@@ -613,7 +530,7 @@ __device__ __forceinline__ void few_down_items(const FewArgs &p, FewSmem &sm, in
     using Src = FewDown<F, S, COLUMNS>;
     const int lane = threadIdx.x & 63, wave = wave_index();
     Src src(p, sm);
-    FewUnits<F, S, Src> run(src, sm);
+    FewUnits<Src> run(src, sm.area, sm.red);
     for (bool have_h = false;;) {
         const int units = COLUMNS ? src.n : src.n * src.blocks;
         const int u0 = COLUMNS ? 0 : share_start(item, units, p.n_down);

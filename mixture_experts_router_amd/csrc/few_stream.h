@@ -198,4 +198,134 @@ __device__ __forceinline__ u32x4 few_i4_operand(uint32_t w) {
     return u32x4{((w << 3) & mask) | base, ((w >> 1) & mask) | base, ((w >> 5) & mask) | base, ((w >> 9) & mask) | base};
 }
 
+// What a step multiplies, out of its slot and the token rows (bf16, MXFP4,
+// NVFP4).
+template <int F>
+struct FewData {
+    u32x4 c[2];
+    uint32_t sc[2];
+    u32x4 x[FewStep<F>::FRAGS];
+};
+
+template <int F>
+__device__ __forceinline__ void few_multiply(const FewData<F> &d, f32x4 (&acc)[2]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if constexpr (F == kFewBf16) {
+            acc[h] = mfma16x16x32(d.c[h], d.x[h], acc[h]);
+        } else {
+#pragma unroll
+            for (int f = 0; f < 4; ++f) acc[h] = mfma16x16x32(few_operand<F>(d.c[h], d.sc[h], f), d.x[4 * h + f], acc[h]);
+        }
+    }
+}
+
+// A workgroup's run of units, each an MFMA tile of sixteen weight rows summed
+// along its steps.  Whole rounds of eight units go a unit to a wave and need no
+// barrier; the units that are left (fewer than eight) are split along K so that
+// no wave is longer at work than it must, and their sums joined.  The order of
+// each unit's sum depends on the run alone.
+//
+// Src says what the units are: S, SLOT, OPS (steps in a ring, bytes of its
+// slots, loads of a step), at(u, v) (the unit's segment of the weights, v or a
+// later one), span(v, a, b) (its steps), rows(u, v), issue(rows, v, step,
+// slot), operand(u, v) (this lane's token data), fetch(slot, step, operand)
+// (out of LDS), multiply(data, step, operand, acc), finish(u, v, sums).
+template <class Src>
+struct FewUnits {
+    static constexpr int S = Src::S, SLOT = Src::SLOT, OPS = Src::OPS, WAVES = 8;
+    const Src &src;
+    uint8_t *ring;
+    f32x4 (*red)[64];                                 // partial sums of the waves
+    int wave, lane;
+    int u0 = 0, um = 0, u1 = 0, KW = 1, UG = 1;      // the run; um: the units that are left, UG at a time
+    int v0 = 0;                                       // its first segment
+    int lu = 0, lv = 0, ls = 0, ls1 = 0, lslot = 0;   // the step to request next (u1: none) and its slot
+    typename Src::Rows rows;
+
+    __device__ __forceinline__ FewUnits(const Src &src, uint8_t *rings, f32x4 (*red)[64])
+        : src(src), ring(rings + wave_index() * S * SLOT), red(red), wave(wave_index()), lane(threadIdx.x & 63) {}
+    // this wave's steps of unit u of segment v
+    __device__ __forceinline__ void part(int u, int v, int &a, int &b) const {
+        src.span(v, a, b);
+        if (u >= um) {
+            const int kw = wave & (KW - 1), n = b - a;
+            b = a + (kw + 1) * n / KW;
+            a += kw * n / KW;
+        }
+    }
+    // the next unit with steps for this wave: u, or one after it (left: u is one of the units that are left)
+    __device__ __forceinline__ void seek(int u, bool left) {
+        for (;; u += left ? UG : WAVES) {
+            if (!left && u >= um) {
+                left = true;
+                u = um + wave / KW;
+            }
+            lu = u1;
+            if (u >= u1) return;
+            lv = src.at(u, lv);
+            part(u, lv, ls, ls1);
+            if (ls < ls1) break;   // not where there are more waves than steps
+        }
+        lu = u;
+        rows = src.rows(u, lv);
+    }
+    __device__ __forceinline__ void request() {
+        src.issue(rows, lv, ls, ring + lslot * SLOT);
+        lslot = lslot + 1 == S ? 0 : lslot + 1;
+        if (++ls == ls1) seek(lu + (lu >= um ? UG : WAVES), lu >= um);
+    }
+    // Requests the first steps of units a .. b - 1, a of segment v, each of at most `steps` steps.
+    __device__ __forceinline__ void start(int a, int b, int v, int steps) {
+        u0 = a;
+        u1 = b;
+        um = b - (b - a) % WAVES;
+        KW = few_kwaves(b - um, steps);
+        UG = WAVES / KW;
+        v0 = lv = v;
+        lslot = 0;
+        seek(u0 + wave, false);
+        for (int i = 0; i < S && lu < u1; ++i) request();
+    }
+    __device__ __forceinline__ void run() {
+        int slot = 0, v = v0;
+        for (int i = u0; i < u1;) {
+            const bool left = i >= um;
+            const int u = i + (left ? wave / KW : wave);
+            f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+            if (uniform(u < u1)) {
+                v = src.at(u, v);
+                const auto x = src.operand(u, v);
+                int a, b;
+                part(u, v, a, b);
+                for (int st = a; st < b; ++st) {
+                    // the ring is full but for this step's successors: S - 1 steps may be in flight
+                    if (lu < u1) few_wait<(S - 1) * OPS>();
+                    else few_wait<0>();
+                    // everything of the step into registers at once, then its slot is free for another
+                    const auto d = src.fetch(ring + slot * SLOT, st, x);
+                    few_lds_done();
+                    if (lu < u1) request();
+                    src.multiply(d, st, x, acc);
+                    slot = slot + 1 == S ? 0 : slot + 1;
+                }
+            }
+            const f32x4 sum = acc[0] + acc[1];
+            if (!left) {
+                src.finish(u, v, sum);
+            } else {
+                red[wave][lane] = sum;
+                __syncthreads();
+                if (uniform(wave < UG && i + wave < u1)) {
+                    f32x4 all = {0.f, 0.f, 0.f, 0.f};
+                    for (int w = 0; w < KW; ++w) all += red[wave * KW + w][lane];
+                    src.finish(i + wave, src.at(i + wave, v0), all);
+                }
+                __syncthreads();
+            }
+            i += left ? UG : WAVES;
+        }
+    }
+};
+
 }  // namespace moe

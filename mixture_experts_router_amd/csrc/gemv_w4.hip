@@ -15,6 +15,7 @@
 // group at a time, and each group's fp32 sum is corrected by the group's token
 // sum: y += scale (sum_k (16 + code) x - (16 + zero) sum_k x).
 #include <algorithm>
+#include <type_traits>
 
 #include "few_stream.h"
 #include "moe_launch.h"
@@ -40,6 +41,7 @@ struct GemvArgs {
     int outs, units;          // y columns; units of 16 weight rows
     int ranges, slices;       // workgroups: ranges x slices
     int geglu, y_fp32;
+    int y_wide;               // rows of y allow stores of four values
 };
 
 struct GemvSmem {
@@ -69,94 +71,208 @@ __device__ __forceinline__ int gemv_row(const GemvArgs &p, int u, int m) {
     return min(16 * u + m, p.N - 1);
 }
 
-// The epilogue of one value per thread: sums of weight row m of unit u and
-// token t (all 64 lanes of a wave call it; m = lane % 16).
+// The epilogue of unit u: lane 16 g + t has the sums of weight rows 4 g + q of
+// the unit and token t.
 template <int F>
-__device__ __forceinline__ void gemv_store(const GemvArgs &p, int u, int m, int t, float sum) {
-    const int n = gemv_row(p, u, m);
+__device__ __forceinline__ void gemv_store(const GemvArgs &p, int u, f32x4 sum) {
+    const int t = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
     if constexpr (F == kFewNv) sum *= *p.global;
-    if (p.bias) sum += *MOE_CHECKED(p.bias + n, 4, p.bias, (size_t)p.N * 4);
-    int col = 16 * u + m;
-    bool on = t < p.T && col < p.outs;
+    if (p.bias) {
+        // uniform addresses in read-only memory, so scalar loads: a vector load would be waited for behind the
+        // ring's, all of which would have to arrive
+        const auto *bias = reinterpret_cast<const __attribute__((address_space(4))) float *>(
+            reinterpret_cast<uintptr_t>(p.bias));
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            float b[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) b[i] = bias[uniform(gemv_row(p, u, 4 * i + q))];
+            sum[q] += g == 0 ? b[0] : g == 1 ? b[1] : g == 2 ? b[2] : b[3];
+        }
+    }
+    int col = 16 * u + 4 * g;
+    bool on = t < p.T;
     if (p.geglu) {
-        const float up = __shfl_down(sum, 8);
-        col = 8 * u + m;
-        on = t < p.T && m < 8 && col < p.outs;
-        sum = gelu_tanh(sum) * up;
+        // gate rows 0..7, up rows 8..15: a gate's up value is 32 lanes above
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const uint32_t b = __float_as_uint(sum[q]);
+            sum[q] = gelu_tanh(sum[q]) * __uint_as_float(__builtin_amdgcn_permlane32_swap(b, b, false, false)[1]);
+        }
+        col = 8 * u + 4 * g;
+        on = on && g < 2;
     }
     if (!on) return;
     const long long at = t * p.ldy + col;
     [[maybe_unused]] const size_t vals = (size_t)((p.T - 1) * p.ldy + p.outs);
-    if (p.y_fp32) *MOE_CHECKED(static_cast<float *>(p.y) + at, 4, p.y, vals * 4) = sum;
-    else *MOE_CHECKED(static_cast<uint16_t *>(p.y) + at, 2, p.y, vals * 2) = (uint16_t)f32_to_bf16_rne(sum);
+    if (p.y_fp32) {
+        float *y = static_cast<float *>(p.y) + at;
+        if (p.y_wide && col + 4 <= p.outs) {
+            *reinterpret_cast<f32x4 *>(MOE_CHECKED(y, 16, p.y, vals * 4)) = sum;
+        } else {
+            for (int q = 0; q < 4 && col + q < p.outs; ++q) *MOE_CHECKED(y + q, 4, p.y, vals * 4) = sum[q];
+        }
+    } else {
+        uint16_t *y = static_cast<uint16_t *>(p.y) + at;
+        if (p.y_wide && col + 4 <= p.outs) {
+            *reinterpret_cast<uint64_t *>(MOE_CHECKED(y, 8, p.y, vals * 2)) =
+                pack_bf16x2(sum[0], sum[1]) | (uint64_t)pack_bf16x2(sum[2], sum[3]) << 32;
+        } else {
+            for (int q = 0; q < 4 && col + q < p.outs; ++q)
+                *MOE_CHECKED(y + q, 2, p.y, vals * 2) = (uint16_t)f32_to_bf16_rne(sum[q]);
+        }
+    }
 }
+
+// The units of a product's range: sixteen weight rows (GEGLU: eight gate rows
+// and the matching eight up rows), steps c0 .. c1 - 1 of them.
+template <int F, int GROUP, bool ZEROS, int S_>
+struct GemvUnits {
+    static constexpr int S = S_, SLOT = GemvSlot<F, GROUP, ZEROS>::SLOT, OPS = GemvSlot<F, GROUP, ZEROS>::OPS;
+    static constexpr int NS = GemvSlot<F, GROUP, ZEROS>::NS, FRAGS = FewStep<F>::FRAGS;
+    static constexpr bool I4 = F == kFewI4;
+    static constexpr int NG = I4 ? 256 / (I4 ? GROUP : 1) : 1;   // groups of a step
+    const GemvArgs &p;
+    const FewLane<F, true> ln;       // NVFP4: K a multiple of 32
+    const int slice, c0, c1;
+    const uint8_t *xs;               // token rows, 16 bytes per fragment, lane group and token
+    const float *xsum;               // INT4: sums of a group and token
+    const int pg, tr;                // INT4: groups of a row; this lane's token
+
+    struct Rows : FewRows {
+        size_t group;                // INT4: first group of this lane's row (MFMA row lane % 16)
+    };
+    struct Operand {
+        const uint8_t *x;
+        uint32_t lo[I4 ? 4 : 1];     // where in its word a scale (zero) lies: the low bits of its address or index
+    };
+    struct I4Data {
+        u32x4 c[2], x[FRAGS], scale[NG], zero[ZEROS ? NG : 1];
+        float xsum[NG];
+    };
+    using Data = std::conditional_t<I4, I4Data, FewData<F>>;
+
+    __device__ __forceinline__ GemvUnits(const GemvArgs &p, int slice, int c0, int c1, const uint8_t *xs, const float *xsum)
+        : p(p), ln(p.K), slice(slice), c0(c0), c1(c1), xs(xs), xsum(xsum), pg(I4 ? p.K / (I4 ? GROUP : 1) : 0),
+          tr(min((int)(threadIdx.x & 15), p.T - 1)) {}
+    __device__ __forceinline__ int at(int, int) const { return 0; }
+    __device__ __forceinline__ void span(int, int &a, int &b) const {
+        a = c0;
+        b = c1;
+    }
+    __device__ __forceinline__ Rows rows(int u, int) const {
+        const int top = p.geglu ? 8 * u : 16 * u, low = p.geglu ? p.outs + top : min(top + 8, p.N - 1);
+        const int ntop = min(7, (p.geglu ? p.outs : p.N) - 1 - top), nlow = p.geglu ? ntop : min(7, p.N - 1 - low);
+        Rows m{ln.rows(p.w + (size_t)top * ln.pitch, p.w + (size_t)low * ln.pitch, p.scales + (size_t)top * ln.spitch,
+                       p.scales + (size_t)low * ln.spitch, ntop, nlow), 0};
+        if constexpr (I4) m.group = (size_t)gemv_row(p, u, ln.r) * pg;
+        return m;
+    }
+    __device__ __forceinline__ void issue(const Rows &m, int, int st, uint8_t *slot) const {
+        const size_t sn = (size_t)p.N * (I4 ? 2 * pg : (int)ln.spitch);
+        ln.issue(m, st, slot, p.w, (size_t)p.N * ln.pitch, p.scales, sn);
+        if constexpr (I4) {
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+                const int j = st * NG + ln.g + 4 * i;
+                const size_t at = m.group + (j < pg ? j : 0);
+                dma4(MOE_CHECKED(p.scales + 2 * (at & ~(size_t)1), 4, p.scales, (sn + 3) & ~(size_t)3), slot + 2048 + 256 * i);
+                if constexpr (ZEROS)
+                    dma4(MOE_CHECKED(p.zeros + (at & ~(size_t)3), 4, p.zeros, ((size_t)p.N * pg + 3) & ~(size_t)3),
+                         slot + 2048 + 256 * (NS + i));
+            }
+        }
+    }
+    __device__ __forceinline__ Operand operand(int u, int) const {
+        Operand o;
+        o.x = xs + (ln.g * p.T + tr) * 16;
+        if constexpr (I4) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) o.lo[q] = (uint32_t)gemv_row(p, u, 4 * ln.g + q) * (uint32_t)pg;
+        } else {
+            o.lo[0] = (uint32_t)reinterpret_cast<uintptr_t>(p.scales) + (uint32_t)gemv_row(p, u, ln.r) * ln.spitch;
+        }
+        return o;
+    }
+    __device__ __forceinline__ Data fetch(const uint8_t *q, int st, const Operand &o) const {
+        Data d;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            d.c[h] = ln.load(q, h);
+            if constexpr (!I4) d.sc[h] = ln.scale(q, st, h, o.lo[0]);
+        }
+        if constexpr (I4) {
+#pragma unroll
+            for (int j = 0; j < NG; ++j) {
+                d.scale[j] = *reinterpret_cast<const u32x4 *>(q + 2048 + 4 * (16 * j + 4 * ln.g));
+                if constexpr (ZEROS) d.zero[j] = *reinterpret_cast<const u32x4 *>(q + 2048 + 256 * NS + 4 * (16 * j + 4 * ln.g));
+                d.xsum[j] = xsum[((st - c0) * NG + j) * p.T + tr];
+            }
+        }
+        const uint8_t *x = o.x + (size_t)(st - c0) * FRAGS * 64 * p.T;
+#pragma unroll
+        for (int f = 0; f < FRAGS; ++f) d.x[f] = *reinterpret_cast<const u32x4 *>(x + f * 64 * p.T);
+        return d;
+    }
+    __device__ __forceinline__ void multiply(const Data &d, int st, const Operand &o, f32x4 (&acc)[2]) const {
+        if constexpr (!I4) {
+            few_multiply<F>(d, acc);
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                u32x4 c = d.c[h];
+                few_transpose(c);
+                f32x4 part;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int f = 4 * h + i, j = f * 32 / GROUP;
+                    if (i * 32 % GROUP == 0) part = f32x4{0.f, 0.f, 0.f, 0.f};
+                    part = mfma16x16x32(few_i4_operand(c[i]), d.x[f], part);
+                    if ((i + 1) * 32 % GROUP) continue;
+                    const int grp = st * NG + j;   // past the row: counts nothing, whatever the words hold
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t at = o.lo[e] + grp, w = grp < pg ? d.scale[j][e] : 0u;
+                        const float s = __uint_as_float(at & 1 ? w & 0xFFFF0000u : w << 16);
+                        const float z = ZEROS ? (float)((d.zero[j][e] >> (8 * (at & 3))) & 0xFFu) : 8.f;
+                        acc[h][e] = fmaf(s, fmaf(-(16.f + z), d.xsum[j], part[e]), acc[h][e]);
+                    }
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void finish(int u, int, const f32x4 &sum) const {
+        if (p.slices == 1) {
+            gemv_store<F>(p, u, sum);
+        } else if ((int)ln.r < p.T) {
+            *reinterpret_cast<f32x4 *>(MOE_CHECKED(p.part + (((size_t)u * p.slices + slice) * p.T + ln.r) * 16 + 4 * ln.g, 16,
+                                                   p.part, (size_t)p.units * p.slices * p.T * 64)) = sum;
+        }
+    }
+};
 
 // S: steps in each wave's ring.
 template <int F, int GROUP, bool ZEROS, int S>
 __global__ __launch_bounds__(kGemvThreads) void gemv_w4_kernel(GemvArgs p) {
     __shared__ GemvSmem sm;
-    using G = GemvSlot<F, GROUP, ZEROS>;
-    constexpr int SLOT = G::SLOT, OPS = G::OPS, FRAGS = FewStep<F>::FRAGS;
-    const int lane = threadIdx.x & 63, wave = wave_index(), r = lane & 15, g = lane >> 4;
-    const int range = blockIdx.x / p.slices, slice = blockIdx.x % p.slices;
+    using Src = GemvUnits<F, GROUP, ZEROS, S>;
+    const int wave = wave_index(), range = blockIdx.x / p.slices, slice = blockIdx.x % p.slices, T = p.T;
     const int nst = few_steps(F, p.K);
     const int c0 = (int)((long long)slice * nst / p.slices), c1 = (int)((long long)(slice + 1) * nst / p.slices);
     const int u0 = (int)((long long)range * p.units / p.ranges), u1 = (int)((long long)(range + 1) * p.units / p.ranges);
-    const int T = p.T, K = p.K, tr = min(r, T - 1);
-    const int KW = few_kwaves(u1 - u0, c1 - c0), UG = kGemvWaves / KW, kw = wave % KW;
-    const int s0 = c0 + kw * (c1 - c0) / KW, s1 = c0 + (kw + 1) * (c1 - c0) / KW;
-    const FewLane<F, true> ln(K);   // NVFP4 rows of 32 K values more or less
-    uint8_t *ring = sm.area + wave * S * SLOT, *xs = sm.area + kGemvWaves * S * SLOT;
-    const int nx = (c1 - c0) * FRAGS * 4 * T;   // 16-byte pieces of the token rows
+    uint8_t *xs = sm.area + kGemvWaves * S * Src::SLOT;
+    const int nx = (c1 - c0) * Src::FRAGS * 4 * T;   // 16-byte pieces of the token rows
     [[maybe_unused]] float *xsum = reinterpret_cast<float *>(xs + (size_t)nx * 16);
-    [[maybe_unused]] const size_t xbytes = (size_t)((T - 1) * p.ldx + K) * 2;
-    const size_t wn = (size_t)p.N * ln.pitch;
-    [[maybe_unused]] const int pg = GROUP ? K / (GROUP ? GROUP : 1) : 0;   // groups of a row
-    const size_t sn = (size_t)p.N * (F == kFewI4 ? 2 * pg : (int)ln.spitch);
-
-    // the step to request next: of unit lu
-    int lu = u0 + wave / KW, ls = s0, lslot = 0;
-    FewRows rows;
-    [[maybe_unused]] size_t lgroup = 0;         // INT4: first group of this lane's row (MFMA row lane % 16)
-    auto point = [&]() {
-        const int top = p.geglu ? 8 * lu : 16 * lu, low = p.geglu ? p.outs + top : min(top + 8, p.N - 1);
-        const int ntop = min(7, (p.geglu ? p.outs : p.N) - 1 - top), nlow = p.geglu ? ntop : min(7, p.N - 1 - low);
-        rows = ln.rows(p.w + (size_t)top * ln.pitch, p.w + (size_t)low * ln.pitch, p.scales + (size_t)top * ln.spitch,
-                       p.scales + (size_t)low * ln.spitch, ntop, nlow);
-        if constexpr (F == kFewI4) lgroup = (size_t)gemv_row(p, lu, r) * pg;
-    };
-    auto request = [&]() {
-        uint8_t *q = ring + lslot * SLOT;
-        ln.issue(rows, ls, q, p.w, wn, p.scales, sn);
-        if constexpr (F == kFewI4) {
-#pragma unroll
-            for (int i = 0; i < G::NS; ++i) {
-                const int j = ls * (256 / GROUP) + g + 4 * i;
-                const size_t at = lgroup + (j < pg ? j : 0);
-                dma4(MOE_CHECKED(p.scales + 2 * (at & ~(size_t)1), 4, p.scales, (sn + 3) & ~(size_t)3), q + 2048 + 256 * i);
-                if constexpr (ZEROS)
-                    dma4(MOE_CHECKED(p.zeros + (at & ~(size_t)3), 4, p.zeros, ((size_t)p.N * pg + 3) & ~(size_t)3),
-                         q + 2048 + 256 * (G::NS + i));
-            }
-        }
-        lslot = lslot + 1 == S ? 0 : lslot + 1;
-        if (++ls == s1) {
-            ls = s0;
-            lu += UG;
-            if (lu < u1) point();
-        }
-    };
-    if (s0 == s1) lu = u1;   // more waves than steps
-    if (lu < u1) {
-        point();
-        for (int i = 0; i < S && lu < u1; ++i) request();
-    }
+    const Src src(p, slice, c0, c1, xs, xsum);
+    FewUnits<Src> run(src, sm.area, sm.red);
+    run.start(u0, u1, 0, c1 - c0);
 
     // token rows of this K range, zero past K
+    [[maybe_unused]] const size_t xbytes = (size_t)((T - 1) * p.ldx + p.K) * 2;
     for (int i = threadIdx.x; i < nx; i += kGemvThreads) {
-        const int t = i % T, fg = i / T, k = few_frag_k<F>(c0 * FRAGS + (fg >> 2), fg & 3);
+        const int t = i % T, fg = i / T, k = few_frag_k<F>(c0 * Src::FRAGS + (fg >> 2), fg & 3);
         u32x4 v = {0u, 0u, 0u, 0u};
-        if (k < K) v = *reinterpret_cast<const u32x4 *>(MOE_CHECKED(p.x + t * p.ldx + k, 16, p.x, xbytes));
+        if (k < p.K) v = *reinterpret_cast<const u32x4 *>(MOE_CHECKED(p.x + t * p.ldx + k, 16, p.x, xbytes));
         *reinterpret_cast<u32x4 *>(xs + (size_t)i * 16) = F == kFewI4 ? few_i4_order(v) : v;
     }
     __syncthreads();
@@ -174,94 +290,7 @@ __global__ __launch_bounds__(kGemvThreads) void gemv_w4_kernel(GemvArgs p) {
         }
         __syncthreads();
     }
-
-    const uint8_t *xl = xs + (g * T + tr) * 16;   // this lane's piece of a token fragment
-    int slot = 0;
-    for (int v0 = u0; v0 < u1; v0 += UG) {
-        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-        [[maybe_unused]] f32x4 half[2] = {acc, acc};   // of the two halves of every step
-        const int u = v0 + wave / KW;
-        if (uniform(u < u1)) {
-            // where in its word a scale (zero) of this lane's rows lies: the low bits of its index
-            [[maybe_unused]] uint32_t lo = 0, low4[4];
-            if constexpr (F == kFewI4) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) low4[q] = (uint32_t)gemv_row(p, u, 4 * g + q) * (uint32_t)pg;
-            } else {
-                lo = (uint32_t)reinterpret_cast<uintptr_t>(p.scales) + (uint32_t)gemv_row(p, u, r) * ln.spitch;
-            }
-            for (int st = s0; st < s1; ++st) {
-                const uint8_t *q = ring + slot * SLOT;
-                if (lu < u1) few_wait<(S - 1) * OPS>();
-                else few_wait<0>();
-                const uint8_t *xq = xl + (size_t)(st - c0) * FRAGS * 64 * T;
-                if constexpr (F == kFewI4) {
-                    f32x4 part = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        u32x4 c = ln.load(q, h);
-                        few_transpose(c);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int f = 4 * h + i, j = f * 32 / GROUP;
-                            part = mfma16x16x32(few_i4_operand(c[i]), *reinterpret_cast<const u32x4 *>(xq + f * 64 * T), part);
-                            if ((i + 1) * 32 % GROUP) continue;
-                            const int grp = st * (256 / GROUP) + j;
-                            if (uniform(grp < pg)) {
-                                const float xv = xsum[(grp - c0 * (256 / GROUP)) * T + tr];
-                                const u32x4 sw = *reinterpret_cast<const u32x4 *>(q + 2048 + 4 * (16 * j + 4 * g));
-                                u32x4 zw = {8u, 8u, 8u, 8u};
-                                if constexpr (ZEROS)
-                                    zw = *reinterpret_cast<const u32x4 *>(q + 2048 + 256 * G::NS + 4 * (16 * j + 4 * g));
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const uint32_t at = low4[e] + grp;
-                                    const float s = __uint_as_float(at & 1 ? sw[e] & 0xFFFF0000u : sw[e] << 16);
-                                    const float z = ZEROS ? (float)((zw[e] >> (8 * (at & 3))) & 0xFFu) : 8.f;
-                                    acc[e] = fmaf(s, fmaf(-(16.f + z), xv, part[e]), acc[e]);
-                                }
-                            }
-                            part = f32x4{0.f, 0.f, 0.f, 0.f};
-                        }
-                    }
-                    few_lds_done();
-                    if (lu < u1) request();
-                } else {
-                    // everything of the step into registers at once, then its slot is free for another
-                    const u32x4 c[2] = {ln.load(q, 0), ln.load(q, 1)};
-                    const uint32_t sc[2] = {ln.scale(q, st, 0, lo), ln.scale(q, st, 1, lo)};
-                    u32x4 xf[FRAGS];
-#pragma unroll
-                    for (int f = 0; f < FRAGS; ++f) xf[f] = *reinterpret_cast<const u32x4 *>(xq + f * 64 * T);
-                    few_lds_done();
-                    if (lu < u1) request();
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            half[h] = mfma16x16x32(few_operand<F>(c[h], sc[h], i), xf[4 * h + i], half[h]);
-                }
-                slot = slot + 1 == S ? 0 : slot + 1;
-            }
-        }
-        if constexpr (F != kFewI4) acc = half[0] + half[1];
-        sm.red[wave][lane] = acc;
-        __syncthreads();
-        // four waves finish a unit (lane 16 (m / 4) + t, element m % 4 of each wave's sums: weight row m, token t)
-        for (int i = wave; i < 4 * UG; i += kGemvWaves) {
-            const int unit = v0 + (i >> 2), m = lane & 15, t = 4 * (i & 3) + (lane >> 4);
-            if (uniform(unit < u1 && 4 * (i & 3) < T)) {
-                float sum = 0.f;
-                for (int v = 0; v < KW; ++v) sum += sm.red[(i >> 2) * KW + v][16 * (m >> 2) + t][m & 3];
-                if (p.slices == 1)
-                    gemv_store<F>(p, unit, m, t, sum);
-                else if (t < T)
-                    *MOE_CHECKED(p.part + (((size_t)unit * p.slices + slice) * T + t) * 16 + m, 4, p.part,
-                                 (size_t)p.units * p.slices * T * 64) = sum;
-            }
-        }
-        __syncthreads();
-    }
+    run.run();
     if (p.slices == 1) return;
     // the last workgroup of the range adds the slices (their stores complete
     // and device-visible before each counts itself done)
@@ -276,14 +305,13 @@ __global__ __launch_bounds__(kGemvThreads) void gemv_w4_kernel(GemvArgs p) {
     }
     __syncthreads();
     if (!uniform(sm.last)) return;
-    for (int i = wave; i < 4 * (u1 - u0); i += kGemvWaves) {
-        const int unit = u0 + (i >> 2), m = lane & 15, t = 4 * (i & 3) + (lane >> 4);
-        if (4 * (i & 3) >= T) continue;
-        float sum = 0.f;
-        for (int s = 0; t < T && s < p.slices; ++s)
-            sum += *MOE_CHECKED(p.part + (((size_t)unit * p.slices + s) * T + t) * 16 + m, 4, p.part,
-                                (size_t)p.units * p.slices * T * 64);
-        gemv_store<F>(p, unit, m, t, sum);
+    const int t = min((int)(threadIdx.x & 15), T - 1), g = (threadIdx.x & 63) >> 4;
+    for (int u = u0 + wave; u < u1; u += kGemvWaves) {
+        f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+        for (int s = 0; s < p.slices; ++s)
+            sum += *reinterpret_cast<const f32x4 *>(MOE_CHECKED(p.part + (((size_t)u * p.slices + s) * T + t) * 16 + 4 * g, 16,
+                                                                p.part, (size_t)p.units * p.slices * T * 64));
+        gemv_store<F>(p, u, sum);
     }
 }
 
@@ -349,6 +377,7 @@ hipError_t launch_gemv_w4(const GemvW4 &l, hipStream_t st) {
     p.slices = g.slices;
     p.geglu = l.geglu;
     p.y_fp32 = l.y_fp32;
+    p.y_wide = l.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(l.y) % (l.y_fp32 ? 16 : 8) == 0;
     if (l.fmt == GemvFormat::kMXFP4) launch_format<kFewMx, 0, false>(p, st);
     else if (l.fmt == GemvFormat::kNVFP4) launch_format<kFewNv, 0, false>(p, st);
     else if (l.group == 32) l.zeros ? launch_format<kFewI4, 32, true>(p, st) : launch_format<kFewI4, 32, false>(p, st);
