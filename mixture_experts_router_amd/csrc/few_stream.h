@@ -193,10 +193,14 @@ __device__ __forceinline__ void few_transpose(u32x4 &c) {
 // mantissa of 16.0 adds exactly its value.  (The offset, and the zero point,
 // leave the fp32 sums with the scale; 16 rather than a larger power of two
 // keeps that cancellation to about two bits.)
-__device__ __forceinline__ u32x4 few_i4_operand(uint32_t w) {
-    constexpr uint32_t mask = 0x00780078u, base = 0x41804180u;
-    return u32x4{((w << 3) & mask) | base, ((w >> 1) & mask) | base, ((w >> 5) & mask) | base, ((w >> 9) & mask) | base};
-}
+struct FewI4 {
+    // in a vector and a scalar register, so that and-or is one instruction (as constants they take two)
+    uint32_t mask = 0x00780078u, base = 0x41804180u;
+    __device__ __forceinline__ FewI4() { asm("" : "+v"(mask), "+s"(base)); }
+    __device__ __forceinline__ u32x4 operand(uint32_t w) const {
+        return u32x4{((w << 3) & mask) | base, ((w >> 1) & mask) | base, ((w >> 5) & mask) | base, ((w >> 9) & mask) | base};
+    }
+};
 
 // What a step multiplies, out of its slot and the token rows (bf16, MXFP4,
 // NVFP4).
@@ -287,6 +291,8 @@ struct FewUnits {
         seek(u0 + wave, false);
         for (int i = 0; i < S && lu < u1; ++i) request();
     }
+    // whether steps are left to request (after start: the ring is full)
+    __device__ __forceinline__ bool more() const { return lu < u1; }
     __device__ __forceinline__ void run() {
         int slot = 0, v = v0;
         for (int i = u0; i < u1;) {

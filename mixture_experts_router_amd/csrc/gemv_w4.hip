@@ -144,7 +144,10 @@ struct GemvUnits {
     };
     struct Operand {
         const uint8_t *x;
-        uint32_t lo[I4 ? 4 : 1];     // where in its word a scale (zero) lies: the low bits of its address or index
+        uint32_t lo;                 // MXFP4, NVFP4: address of this lane's scale row modulo 4
+        // INT4: byte selectors of the scales of even and odd groups in their words, as fp32; bit offset of a zero
+        uint32_t even[4], odd[4], zero[4];
+        FewI4 codes;
     };
     struct I4Data {
         u32x4 c[2], x[FRAGS], scale[NG], zero[ZEROS ? NG : 1];
@@ -175,7 +178,8 @@ struct GemvUnits {
 #pragma unroll
             for (int i = 0; i < NS; ++i) {
                 const int j = st * NG + ln.g + 4 * i;
-                const size_t at = m.group + (j < pg ? j : 0);
+                // past the row: another scale of this row, of a group of the same parity if there is one
+                const size_t at = m.group + (j < pg ? j : (j & 1) < pg ? j & 1 : 0);
                 dma4(MOE_CHECKED(p.scales + 2 * (at & ~(size_t)1), 4, p.scales, (sn + 3) & ~(size_t)3), slot + 2048 + 256 * i);
                 if constexpr (ZEROS)
                     dma4(MOE_CHECKED(p.zeros + (at & ~(size_t)3), 4, p.zeros, ((size_t)p.N * pg + 3) & ~(size_t)3),
@@ -188,9 +192,16 @@ struct GemvUnits {
         o.x = xs + (ln.g * p.T + tr) * 16;
         if constexpr (I4) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) o.lo[q] = (uint32_t)gemv_row(p, u, 4 * ln.g + q) * (uint32_t)pg;
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t at = (uint32_t)gemv_row(p, u, 4 * ln.g + q) * (uint32_t)pg;
+                constexpr uint32_t half[2] = {0x05040c0cu, 0x07060c0cu};   // of the word, in the upper half of an fp32
+                o.even[q] = half[at & 1];
+                // one group in a row: an odd one is past its end, and its word may hold another row's scale
+                o.odd[q] = pg == 1 ? 0x0c0c0c0cu : half[~at & 1];
+                o.zero[q] = 8 * at;
+            }
         } else {
-            o.lo[0] = (uint32_t)reinterpret_cast<uintptr_t>(p.scales) + (uint32_t)gemv_row(p, u, ln.r) * ln.spitch;
+            o.lo = (uint32_t)reinterpret_cast<uintptr_t>(p.scales) + (uint32_t)gemv_row(p, u, ln.r) * ln.spitch;
         }
         return o;
     }
@@ -199,7 +210,7 @@ struct GemvUnits {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             d.c[h] = ln.load(q, h);
-            if constexpr (!I4) d.sc[h] = ln.scale(q, st, h, o.lo[0]);
+            if constexpr (!I4) d.sc[h] = ln.scale(q, st, h, o.lo);
         }
         if constexpr (I4) {
 #pragma unroll
@@ -227,14 +238,13 @@ struct GemvUnits {
                 for (int i = 0; i < 4; ++i) {
                     const int f = 4 * h + i, j = f * 32 / GROUP;
                     if (i * 32 % GROUP == 0) part = f32x4{0.f, 0.f, 0.f, 0.f};
-                    part = mfma16x16x32(few_i4_operand(c[i]), d.x[f], part);
+                    part = mfma16x16x32(o.codes.operand(c[i]), d.x[f], part);
                     if ((i + 1) * 32 % GROUP) continue;
-                    const int grp = st * NG + j;   // past the row: counts nothing, whatever the words hold
+                    // (past the row the tokens are zero: a scale of this row times zero)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const uint32_t at = o.lo[e] + grp, w = grp < pg ? d.scale[j][e] : 0u;
-                        const float s = __uint_as_float(at & 1 ? w & 0xFFFF0000u : w << 16);
-                        const float z = ZEROS ? (float)((d.zero[j][e] >> (8 * (at & 3))) & 0xFFu) : 8.f;
+                        const float s = __uint_as_float(__builtin_amdgcn_perm(d.scale[j][e], 0u, j & 1 ? o.odd[e] : o.even[e]));
+                        const float z = ZEROS ? (float)((d.zero[j][e] >> ((o.zero[e] + 8 * (st * NG + j)) & 31)) & 0xFFu) : 8.f;
                         acc[h][e] = fmaf(s, fmaf(-(16.f + z), d.xsum[j], part[e]), acc[h][e]);
                     }
                 }
@@ -265,16 +275,24 @@ __global__ __launch_bounds__(kGemvThreads) void gemv_w4_kernel(GemvArgs p) {
     [[maybe_unused]] float *xsum = reinterpret_cast<float *>(xs + (size_t)nx * 16);
     const Src src(p, slice, c0, c1, xs, xsum);
     FewUnits<Src> run(src, sm.area, sm.red);
-    run.start(u0, u1, 0, c1 - c0);
 
-    // token rows of this K range, zero past K
+    // token rows of this K range, zero past K: requested before the weights, so that they arrive first
     [[maybe_unused]] const size_t xbytes = (size_t)((T - 1) * p.ldx + p.K) * 2;
     for (int i = threadIdx.x; i < nx; i += kGemvThreads) {
         const int t = i % T, fg = i / T, k = few_frag_k<F>(c0 * Src::FRAGS + (fg >> 2), fg & 3);
-        u32x4 v = {0u, 0u, 0u, 0u};
-        if (k < p.K) v = *reinterpret_cast<const u32x4 *>(MOE_CHECKED(p.x + t * p.ldx + k, 16, p.x, xbytes));
-        *reinterpret_cast<u32x4 *>(xs + (size_t)i * 16) = F == kFewI4 ? few_i4_order(v) : v;
+        if (k < p.K)
+            dma16<false>(MOE_CHECKED(p.x + t * p.ldx + k, 16, p.x, xbytes), xs + (size_t)(i - (threadIdx.x & 63)) * 16);
+        else
+            *reinterpret_cast<u32x4 *>(xs + (size_t)i * 16) = u32x4{0u, 0u, 0u, 0u};
     }
+    run.start(u0, u1, 0, c1 - c0);
+    if (run.more()) few_wait<S * Src::OPS>();   // the ring's S steps are behind them
+    else few_wait<0>();
+    if constexpr (F == kFewI4)
+        for (int i = threadIdx.x; i < nx; i += kGemvThreads) {
+            u32x4 *v = reinterpret_cast<u32x4 *>(xs + (size_t)i * 16);
+            *v = few_i4_order(*v);
+        }
     __syncthreads();
     if constexpr (F == kFewI4) {
         constexpr int per = GROUP / 8;   // 16-byte pieces of one group and token, at stride 16 T
@@ -315,9 +333,8 @@ __global__ __launch_bounds__(kGemvThreads) void gemv_w4_kernel(GemvArgs p) {
     }
 }
 
-// Steps in a ring: the deep one where it leaves the token rows room, else the
-// shallow one.
-constexpr int kGemvDeep = 6, kGemvShallow = 3;
+// Steps in a ring: the deepest that leaves the token rows room.
+constexpr int kGemvDeep = 6, kGemvMiddle = 4, kGemvShallow = 3;
 
 // LDS bytes that `steps` steps of token rows (and INT4's token sums) take.
 size_t gemv_x_bytes(int T, int steps) { return (size_t)steps * 512 * T + (size_t)steps * 32 * T; }
@@ -328,10 +345,10 @@ void launch_format(const GemvArgs &p, hipStream_t st) {
     constexpr int slot = GemvSlot<F, GROUP, ZEROS>::SLOT;
     const dim3 grid(p.ranges * p.slices), block(kGemvThreads);
     const int steps = (few_steps(F, p.K) + p.slices - 1) / p.slices;
-    if (gemv_x_bytes(p.T, steps) + gemv_ring_bytes(slot, kGemvDeep) <= (size_t)kGemvArea)
-        gemv_w4_kernel<F, GROUP, ZEROS, kGemvDeep><<<grid, block, 0, st>>>(p);
-    else
-        gemv_w4_kernel<F, GROUP, ZEROS, kGemvShallow><<<grid, block, 0, st>>>(p);
+    auto fits = [&](int s) { return gemv_x_bytes(p.T, steps) + gemv_ring_bytes(slot, s) <= (size_t)kGemvArea; };
+    if (fits(kGemvDeep)) gemv_w4_kernel<F, GROUP, ZEROS, kGemvDeep><<<grid, block, 0, st>>>(p);
+    else if (fits(kGemvMiddle)) gemv_w4_kernel<F, GROUP, ZEROS, kGemvMiddle><<<grid, block, 0, st>>>(p);
+    else gemv_w4_kernel<F, GROUP, ZEROS, kGemvShallow><<<grid, block, 0, st>>>(p);
 }
 
 }  // namespace
