@@ -415,8 +415,8 @@ int moe_gemv_w4(const moe_w4_shape *s, const uint16_t *x, const uint8_t *w, cons
                 const uint8_t *zeros, const float *bias, void *y, void *ws, size_t ws_bytes,
                 moe_stream_t stream);
 
-/* Workspace bytes moe_gemv_w4 needs for this shape, with zeros or without (0:
- * none needed, or an invalid shape). */
+/* Workspace bytes moe_gemv_w4 needs for this shape (0: none needed, or an
+ * invalid shape). */
 size_t moe_gemv_w4_workspace_bytes(const moe_w4_shape *s);
 
 /* Workspace bytes moe_forward needs for this shape; 0 for an invalid or

@@ -230,12 +230,6 @@ moe::GemvFormat gemv_format(const moe_w4_shape *s) {
                                      : (s->w_format == MOE_W_NVFP4 ? moe::GemvFormat::kNVFP4 : moe::GemvFormat::kMXFP4);
 }
 
-size_t gemv_ws(const moe_w4_shape *s, bool zeros) {
-    const size_t part = moe::gemv_part_bytes(
-        moe::gemv_plan(gemv_format(s), s->group, zeros, s->T, s->N, s->K, s->flags & MOE_GEMV_GEGLU), s->T);
-    return part ? MOE_FEW_ZERO_BYTES + round_up(part) : 0;
-}
-
 int hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 
 // Device address of `scratch` on each device, looked up once per device
@@ -613,8 +607,8 @@ int moe_forward_few(const moe_shape *s, const uint16_t *x, const uint16_t *w_rou
 
 size_t moe_gemv_w4_workspace_bytes(const moe_w4_shape *s) {
     if (check_w4(s) != MOE_OK) return 0;
-    const size_t a = gemv_ws(s, false), b = s->w_format == MOE_W_INT4 ? gemv_ws(s, true) : 0;
-    return a > b ? a : b;
+    const size_t part = moe::gemv_part_bytes(moe::gemv_plan(s->N, s->K, s->flags & MOE_GEMV_GEGLU), s->T);
+    return part ? MOE_FEW_ZERO_BYTES + round_up(part) : 0;
 }
 
 int moe_gemv_w4(const moe_w4_shape *s, const uint16_t *x, const uint8_t *w, const uint8_t *scales,
@@ -626,7 +620,7 @@ int moe_gemv_w4(const moe_w4_shape *s, const uint16_t *x, const uint8_t *w, cons
     if (!x || !w || !scales || !y || !al16(x) || !al16(w)) return MOE_ERR_INVALID_ARGUMENT;
     if (!al4(scales) || (zeros && (!i4 || !al4(zeros))) || (bias && !al4(bias))) return MOE_ERR_INVALID_ARGUMENT;
     if (reinterpret_cast<uintptr_t>(y) & (y_fp32 ? 3u : 1u)) return MOE_ERR_INVALID_ARGUMENT;
-    const size_t need = moe_gemv_w4_workspace_bytes(s);   // with or without zeros
+    const size_t need = moe_gemv_w4_workspace_bytes(s);
     if (need && (!ws || ws_bytes < need || !al16(ws))) return MOE_ERR_WORKSPACE;
     moe::GemvW4 l{};
     l.x = x;

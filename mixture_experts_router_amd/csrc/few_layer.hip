@@ -294,9 +294,9 @@ struct FewOperand {
         : x(x), ln(ln), lo((ln.r & 7) * ln.spitch) {}
 };
 
-// A step out of its slot and the token rows of Src.
+// A step out of its slot and (token step xst) the token rows of Src.
 template <int F, class Src>
-__device__ __forceinline__ FewData<F> few_fetch(const Src &src, const uint8_t *q, int st, const FewOperand<F> &o) {
+__device__ __forceinline__ FewData<F> few_fetch(const Src &src, const uint8_t *q, int st, int xst, const FewOperand<F> &o) {
     FewData<F> d;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -305,16 +305,17 @@ __device__ __forceinline__ FewData<F> few_fetch(const Src &src, const uint8_t *q
         if constexpr (FewStep<F>::SOPS > 0) d.sc[h] = o.ln.scale(q, st, h, o.lo);
     }
 #pragma unroll
-    for (int f = 0; f < FewStep<F>::FRAGS; ++f) d.x[f] = src.frag(o.x, st, f);
+    for (int f = 0; f < FewStep<F>::FRAGS; ++f) d.x[f] = src.frag(o.x, xst, f);
     return d;
 }
 
 // Gate/up units of eight h columns: the MFMA's rows are the unit's eight gate
 // rows and the matching eight up rows.
-template <int F, int S_, bool XL>
+template <int F, int S_, int WINDOW_>
 struct FewGateUp {
-    static constexpr int S = S_, SLOT = FewStep<F>::SLOT, OPS = FewStep<F>::OPS;
+    static constexpr int S = S_, SLOT = FewStep<F>::SLOT, OPS = FewStep<F>::OPS, WINDOW = WINDOW_;
     using Rows = FewRows;
+    using Operand = FewOperand<F>;
     const FewArgs &p;
     FewSmem &sm;
     const bool shared;
@@ -344,26 +345,25 @@ struct FewGateUp {
     __device__ __forceinline__ void issue(const FewRows &m, int v, int st, uint8_t *slot) const {
         lane(v).issue(m, st, slot, weights(v), weight_bytes(v), scales(v), scale_bytes(v));
     }
-    __device__ __forceinline__ FewData<F> fetch(const uint8_t *q, int st, const FewOperand<F> &o) const {
-        return few_fetch<F>(*this, q, st, o);
+    __device__ __forceinline__ FewData<F> fetch(const uint8_t *q, int st, int xst, const FewOperand<F> &o) const {
+        return few_fetch<F>(*this, q, st, xst, o);
     }
     __device__ __forceinline__ void multiply(const FewData<F> &d, int, const FewOperand<F> &, f32x4 (&acc)[2]) const {
         few_multiply<F>(d, acc);
     }
-    // XL: the token rows are in LDS, every fragment as 16 bytes per (g, token)
+    __device__ __forceinline__ uint8_t *tokens(int buffer) const {
+        return sm.area + kFewWaves * S * SLOT + (size_t)buffer * WINDOW * FewStep<F>::FRAGS * 64 * p.T;
+    }
     __device__ __forceinline__ FewOperand<F> operand(int, int) const {
-        const int t = min((int)ln.r, p.T - 1);
-        if constexpr (XL) return {sm.area + kFewWaves * S * SLOT + (ln.g * p.T + t) * 16, ln};
-        return {reinterpret_cast<const uint8_t *>(p.x + (size_t)t * p.H), ln};
+        return {tokens(0) + (ln.g * p.T + min((int)ln.r, p.T - 1)) * 16, ln};
     }
-    __device__ __forceinline__ u32x4 frag(const uint8_t *x, int st, int i) const {
-        const int f = st * FewStep<F>::FRAGS + i;
-        if constexpr (XL) return *reinterpret_cast<const u32x4 *>(x + 64 * f * p.T);
-        const int k = few_frag_k<F>(f, ln.g);
-        const u32x4 v =
-            *reinterpret_cast<const u32x4 *>(MOE_CHECKED(x + 2 * (k < p.H ? k : 0), 16, p.x, (size_t)p.T * p.H * 2));
-        return k < p.H ? v : u32x4{0u, 0u, 0u, 0u};
+    __device__ __forceinline__ u32x4 frag(const uint8_t *x, int xst, int i) const {
+        return *reinterpret_cast<const u32x4 *>(x + 64 * (xst * FewStep<F>::FRAGS + i) * p.T);
     }
+    __device__ __forceinline__ void stage(int a, int b, int buffer) const {
+        few_request_x<F, kFewThreads>(p.x, p.H, p.T, p.H, a * FewStep<F>::FRAGS, b * FewStep<F>::FRAGS, tokens(buffer));
+    }
+    __device__ __forceinline__ void staged(int, int, int) const {}
     // Lane 16 g + t, element q of the sums is weight row 4 g + q, token t: gate rows 0..7, up rows 8..15, so a
     // gate's up value is 32 lanes above.
     __device__ __forceinline__ void finish(int u, int v, const f32x4 &acc) const {
@@ -387,10 +387,10 @@ struct FewGateUp {
     }
 };
 
-template <int F, int S, bool XL>
+template <int F, int S, int WINDOW>
 __device__ __forceinline__ void few_gateup(const FewArgs &p, FewSmem &sm, bool shared, int units, int item) {
-    const FewGateUp<F, S, XL> src(p, sm, shared);
-    FewUnits<FewGateUp<F, S, XL>> run(src, sm.area, sm.red);
+    const FewGateUp<F, S, WINDOW> src(p, sm, shared);
+    FewUnits<FewGateUp<F, S, WINDOW>> run(src, sm.area, sm.red);
     const int u0 = share_start(item, units, p.n_gu);
     run.start(u0, share_start(item + 1, units, p.n_gu), u0 / src.per, few_steps(F, p.H));
     run.run();
@@ -411,8 +411,9 @@ __device__ __forceinline__ void few_gateup(const FewArgs &p, FewSmem &sm, bool s
 // one before h exists.
 template <int F, int S_, bool COLUMNS>
 struct FewDown {
-    static constexpr int S = S_, SLOT = FewStep<F>::SLOT, OPS = FewStep<F>::OPS;
+    static constexpr int S = S_, SLOT = FewStep<F>::SLOT, OPS = FewStep<F>::OPS, WINDOW = 0;
     using Rows = FewRows;
+    using Operand = FewOperand<F>;
     static constexpr int KS = FewStep<F>::K;
     static constexpr int H_BYTES = kFewArea - kFewWaves * S * SLOT;   // LDS for rows of h
     const FewArgs &p;
@@ -467,8 +468,8 @@ struct FewDown {
     __device__ __forceinline__ void issue(const FewRows &m, int v, int st, uint8_t *slot) const {
         lane(v).issue(m, st, slot, weights(v), weight_bytes(v), scales(v), scale_bytes(v));
     }
-    __device__ __forceinline__ FewData<F> fetch(const uint8_t *q, int st, const FewOperand<F> &o) const {
-        return few_fetch<F>(*this, q, st, o);
+    __device__ __forceinline__ FewData<F> fetch(const uint8_t *q, int st, int xst, const FewOperand<F> &o) const {
+        return few_fetch<F>(*this, q, st, xst, o);
     }
     __device__ __forceinline__ void multiply(const FewData<F> &d, int, const FewOperand<F> &, f32x4 (&acc)[2]) const {
         few_multiply<F>(d, acc);
@@ -609,8 +610,8 @@ __device__ __forceinline__ void few_combine(const FewArgs &p, const FewSmem &sm,
     *MOE_CHECKED(p.out + i, 2, p.out, (size_t)p.T * p.H * 2) = (uint16_t)f32_to_bf16_rne(sum);
 }
 
-// S: steps in each wave's ring.  XL: the token rows fit the LDS next to the rings.
-template <int F, int S, bool XL>
+// S: steps in each wave's ring.  WINDOW: of the token rows in gate/up (FewUnits).
+template <int F, int S, int WINDOW>
 __global__ __launch_bounds__(kFewThreads) void few_layer_kernel(FewArgs p) {
     __shared__ FewSmem sm;
     if (threadIdx.x == 0) sm.ticket = (int)ctr_ticket(p, kRouter);
@@ -635,7 +636,7 @@ __global__ __launch_bounds__(kFewThreads) void few_layer_kernel(FewArgs p) {
         sm.ticket = (int)a;
         sm.down = (int)b;
     }
-    if constexpr (XL) few_stage_x<F>(p, sm.area + kFewWaves * S * FewStep<F>::SLOT);
+    if constexpr (WINDOW == 0) few_stage_x<F>(p, sm.area + kFewWaves * S * FewStep<F>::SLOT);
     __syncthreads();
     int t = uniform(sm.ticket);
     const int d = uniform(sm.down);
@@ -643,7 +644,7 @@ __global__ __launch_bounds__(kFewThreads) void few_layer_kernel(FewArgs p) {
     for (;;) {
         const bool share = (uint32_t)t < (uint32_t)p.n_gu;
         if (share && p.I_sh) {   // needs no routing
-            few_gateup<F, S, XL>(p, sm, true, p.I_sh / 8, t);
+            few_gateup<F, S, WINDOW>(p, sm, true, p.I_sh / 8, t);
             __syncthreads();   // the sums in LDS are free
         }
         if (!selected) few_select(p, sm, t == 0);
@@ -651,7 +652,7 @@ __global__ __launch_bounds__(kFewThreads) void few_layer_kernel(FewArgs p) {
         if (!share) break;
         // the next ticket, early: none is left unless a workgroup has not started yet
         if (threadIdx.x == 0) sm.ticket = (int)ctr_ticket(p, kGateUp);
-        few_gateup<F, S, XL>(p, sm, false, uniform(sm.n_experts) * (p.I / 8), t);
+        few_gateup<F, S, WINDOW>(p, sm, false, uniform(sm.n_experts) * (p.I / 8), t);
         publish(p, kGateUp, p.n_gu);
         t = uniform(sm.ticket);
         __syncthreads();
@@ -684,9 +685,8 @@ __global__ __launch_bounds__(kFewThreads) void few_layer_kernel(FewArgs p) {
 }
 
 // Steps in a ring: the deepest that leaves the token rows room (bf16 or 4-bit,
-// by slot size); the last with rows that are too long for any, read from
-// global memory.
-constexpr int kRings = 4, kRing[2][kRings + 1] = {{7, 5, 4, 3, 5}, {6, 5, 4, 2, 5}};
+// by slot size), else the one that leaves room for windows of them.
+constexpr int kRings = 3, kRing[2][kRings + 1] = {{7, 5, 3, 6}, {6, 4, 2, 4}}, kWindow[2] = {8, 4};
 
 struct FewPlan {
     int ring;      // of kRing
@@ -715,11 +715,12 @@ FewPlan few_plan(int f, int T, int H, int k, int I, int I_sh) {
 
 template <int F, int R = 0>
 void launch_format(const FewArgs &p, int ring, int blocks, hipStream_t st) {
-    constexpr int S = kRing[F != kFewBf16][R];
+    constexpr int S = kRing[F != kFewBf16][R], W = R == kRings ? kWindow[F != kFewBf16] : 0;
+    static_assert(2 * W * FewStep<F>::FRAGS * 64 * kFewTokens <= kFewArea - kFewWaves * S * FewStep<F>::SLOT, "windows");
     static_assert((kFewArea - kFewWaves * S * FewStep<F>::SLOT) / kFewTokens >= 16 + FewStep<F>::K * 2,
                   "a segment is one step or more");
     if (ring == R) {
-        few_layer_kernel<F, S, R != kRings><<<blocks, kFewThreads, 0, st>>>(p);
+        few_layer_kernel<F, S, W><<<blocks, kFewThreads, 0, st>>>(p);
         return;
     }
     if constexpr (R < kRings) launch_format<F, R + 1>(p, ring, blocks, st);

@@ -230,11 +230,20 @@ __device__ __forceinline__ void few_multiply(const FewData<F> &d, f32x4 (&acc)[2
 // no wave is longer at work than it must, and their sums joined.  The order of
 // each unit's sum depends on the run alone.
 //
+// Token rows are in LDS, whole, before run() (WINDOW 0), or, where that leaves
+// the rings too little room, come in windows of up to WINDOW steps: all waves
+// go through the same windows, the next of which is on its way to a second
+// buffer meanwhile, and a barrier separates them.  Then all units go a unit to
+// a wave.
+//
 // Src says what the units are: S, SLOT, OPS (steps in a ring, bytes of its
-// slots, loads of a step), at(u, v) (the unit's segment of the weights, v or a
-// later one), span(v, a, b) (its steps), rows(u, v), issue(rows, v, step,
-// slot), operand(u, v) (this lane's token data), fetch(slot, step, operand)
-// (out of LDS), multiply(data, step, operand, acc), finish(u, v, sums).
+// slots, loads of a step), WINDOW, at(u, v) (the unit's segment of the
+// weights, v or a later one), span(v, a, b) (its steps), rows(u, v),
+// issue(rows, v, step, slot), operand(u, v) (this lane's token data),
+// fetch(slot, step, token step, operand) (out of LDS), multiply(data, step,
+// operand, acc), finish(u, v, sums); with windows stage(a, b, buffer) (requests
+// the token rows of steps a .. b - 1) and staged(a, b, buffer) (they are here:
+// each thread's own).
 template <class Src>
 struct FewUnits {
     static constexpr int S = Src::S, SLOT = Src::SLOT, OPS = Src::OPS, WAVES = 8;
@@ -245,6 +254,7 @@ struct FewUnits {
     int u0 = 0, um = 0, u1 = 0, KW = 1, UG = 1;      // the run; um: the units that are left, UG at a time
     int v0 = 0;                                       // its first segment
     int lu = 0, lv = 0, ls = 0, ls1 = 0, lslot = 0;   // the step to request next (u1: none) and its slot
+    int c0 = 0, c1 = 0, NW = 1;                       // windows: of steps c0 .. c1 - 1
     typename Src::Rows rows;
 
     __device__ __forceinline__ FewUnits(const Src &src, uint8_t *rings, f32x4 (*red)[64])
@@ -283,8 +293,13 @@ struct FewUnits {
     __device__ __forceinline__ void start(int a, int b, int v, int steps) {
         u0 = a;
         u1 = b;
-        um = b - (b - a) % WAVES;
-        KW = few_kwaves(b - um, steps);
+        um = Src::WINDOW ? b : b - (b - a) % WAVES;
+        KW = Src::WINDOW ? 1 : few_kwaves(b - um, steps);
+        if constexpr (Src::WINDOW > 0) {
+            src.span(v, c0, c1);
+            NW = (c1 - c0 + Src::WINDOW - 1) / Src::WINDOW;
+            if (a < b) src.stage(c0, c0 + (c1 - c0) / NW, 0);
+        }
         UG = WAVES / KW;
         v0 = lv = v;
         lslot = 0;
@@ -293,32 +308,59 @@ struct FewUnits {
     }
     // whether steps are left to request (after start: the ring is full)
     __device__ __forceinline__ bool more() const { return lu < u1; }
+    // Steps a .. b - 1 of this wave's unit, whose token rows begin with token step x0.
+    __device__ __forceinline__ void steps(int a, int b, int x0, const typename Src::Operand &x, int &slot, f32x4 (&acc)[2]) {
+        for (int st = a; st < b; ++st) {
+            // the ring is full but for this step's successors: S - 1 steps may be in flight
+            if (lu < u1) few_wait<(S - 1) * OPS>();
+            else few_wait<0>();
+            // everything of the step into registers at once, then its slot is free for another
+            const auto d = src.fetch(ring + slot * SLOT, st, x0 + st - a, x);
+            few_lds_done();
+            if (lu < u1) request();
+            src.multiply(d, st, x, acc);
+            slot = slot + 1 == S ? 0 : slot + 1;
+        }
+    }
+    // Window w of a round is here, and all waves are done with the one before; the next is requested (last: no).
+    __device__ __forceinline__ void next_window(int n, int w, bool last) const {
+        static_assert(S * OPS <= 63 && Src::WINDOW / 2 * OPS <= 63, "the counter of outstanding loads");
+        // behind its requests: the ring's S steps, later a step's for each of the window before (no fewer than
+        // half a WINDOW: windows are as even as whole steps allow)
+        if (lu >= u1) few_wait<0>();
+        else if (n == 0) few_wait<S * OPS>();
+        else few_wait<Src::WINDOW / 2 * OPS>();
+        const int len = c1 - c0;
+        src.staged(c0 + w * len / NW, c0 + (w + 1) * len / NW, n & 1);
+        __syncthreads();
+        if (last) return;
+        const int m = w + 1 == NW ? 0 : w + 1;
+        src.stage(c0 + m * len / NW, c0 + (m + 1) * len / NW, (n + 1) & 1);
+    }
     __device__ __forceinline__ void run() {
         int slot = 0, v = v0;
+        [[maybe_unused]] int n = 0;   // windows so far
         for (int i = u0; i < u1;) {
             const bool left = i >= um;
             const int u = i + (left ? wave / KW : wave);
+            const bool on = uniform(u < u1);
             f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-            if (uniform(u < u1)) {
+            if constexpr (Src::WINDOW > 0) {
+                typename Src::Operand x = src.operand(on ? u : u0, v = src.at(on ? u : u1 - 1, v));
+                for (int w = 0; w < NW; ++w, ++n) {
+                    next_window(n, w, w + 1 == NW && i + WAVES >= u1);
+                    const int a = c0 + w * (c1 - c0) / NW, b = c0 + (w + 1) * (c1 - c0) / NW;
+                    if (on) steps(a, b, (n & 1) * Src::WINDOW, x, slot, acc);
+                }
+            } else if (on) {
                 v = src.at(u, v);
-                const auto x = src.operand(u, v);
                 int a, b;
                 part(u, v, a, b);
-                for (int st = a; st < b; ++st) {
-                    // the ring is full but for this step's successors: S - 1 steps may be in flight
-                    if (lu < u1) few_wait<(S - 1) * OPS>();
-                    else few_wait<0>();
-                    // everything of the step into registers at once, then its slot is free for another
-                    const auto d = src.fetch(ring + slot * SLOT, st, x);
-                    few_lds_done();
-                    if (lu < u1) request();
-                    src.multiply(d, st, x, acc);
-                    slot = slot + 1 == S ? 0 : slot + 1;
-                }
+                steps(a, b, a, src.operand(u, v), slot, acc);
             }
             const f32x4 sum = acc[0] + acc[1];
             if (!left) {
-                src.finish(u, v, sum);
+                if (on) src.finish(u, v, sum);
             } else {
                 red[wave][lane] = sum;
                 __syncthreads();
@@ -333,5 +375,17 @@ struct FewUnits {
         }
     }
 };
+
+// Requests 16-byte pieces of T token rows (row stride ld) for fragments f0 ..
+// f1 - 1 into LDS: in fragment, lane group, token order, zero past K.
+template <int F, int THREADS>
+__device__ __forceinline__ void few_request_x(const uint16_t *x, long long ld, int T, int K, int f0, int f1, uint8_t *dst) {
+    [[maybe_unused]] const size_t bytes = (size_t)((T - 1) * ld + K) * 2;
+    for (int i = threadIdx.x; i < (f1 - f0) * 4 * T; i += THREADS) {
+        const int t = i % T, fg = i / T, k = few_frag_k<F>(f0 + (fg >> 2), fg & 3);
+        if (k < K) dma16<false>(MOE_CHECKED(x + t * ld + k, 16, x, bytes), dst + (size_t)(i - (threadIdx.x & 63)) * 16);
+        else *reinterpret_cast<u32x4 *>(dst + (size_t)i * 16) = u32x4{0u, 0u, 0u, 0u};
+    }
+}
 
 }  // namespace moe

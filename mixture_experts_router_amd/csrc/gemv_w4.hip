@@ -12,8 +12,9 @@
 //
 // INT4: W = scale (code - zero) with one scale and zero per group of 32, 64 or
 // 128 K values.  The matrix cores multiply the exact values 16 + code, one
-// group at a time, and each group's fp32 sum is corrected by the group's token
-// sum: y += scale (sum_k (16 + code) x - (16 + zero) sum_k x).
+// group at a time: y = sum over groups of scale sum_k (16 + code) x
+// - sum over groups of scale (16 + zero) sum_k x, the second of which is an
+// fp32 matrix product over the groups.
 #include <algorithm>
 #include <type_traits>
 
@@ -126,17 +127,18 @@ __device__ __forceinline__ void gemv_store(const GemvArgs &p, int u, f32x4 sum) 
 
 // The units of a product's range: sixteen weight rows (GEGLU: eight gate rows
 // and the matching eight up rows), steps c0 .. c1 - 1 of them.
-template <int F, int GROUP, bool ZEROS, int S_>
+template <int F, int GROUP, bool ZEROS, int S_, int WINDOW_>
 struct GemvUnits {
+    static constexpr int WINDOW = WINDOW_;
     static constexpr int S = S_, SLOT = GemvSlot<F, GROUP, ZEROS>::SLOT, OPS = GemvSlot<F, GROUP, ZEROS>::OPS;
     static constexpr int NS = GemvSlot<F, GROUP, ZEROS>::NS, FRAGS = FewStep<F>::FRAGS;
     static constexpr bool I4 = F == kFewI4;
+    static constexpr uint32_t kOnes = 0x3F803F80u;               // bf16
     static constexpr int NG = I4 ? 256 / (I4 ? GROUP : 1) : 1;   // groups of a step
     const GemvArgs &p;
     const FewLane<F, true> ln;       // NVFP4: K a multiple of 32
     const int slice, c0, c1;
-    const uint8_t *xs;               // token rows, 16 bytes per fragment, lane group and token
-    const float *xsum;               // INT4: sums of a group and token
+    uint8_t *const xs;               // token rows, 16 bytes per fragment, lane group and token
     const int pg, tr;                // INT4: groups of a row; this lane's token
 
     struct Rows : FewRows {
@@ -145,18 +147,19 @@ struct GemvUnits {
     struct Operand {
         const uint8_t *x;
         uint32_t lo;                 // MXFP4, NVFP4: address of this lane's scale row modulo 4
-        // INT4: byte selectors of the scales of even and odd groups in their words, as fp32; bit offset of a zero
-        uint32_t even[4], odd[4], zero[4];
+        // INT4: byte selectors of the scales in their words, as fp32: of rows 4 g + q, even and odd groups, and of
+        // the words this lane loads; bit offset of its zeros in theirs
+        uint32_t even[4], odd[4], own, zero;
         FewI4 codes;
     };
     struct I4Data {
-        u32x4 c[2], x[FRAGS], scale[NG], zero[ZEROS ? NG : 1];
-        float xsum[NG];
+        u32x4 c[2], x[FRAGS], scale[NG];
+        uint32_t own[NS + 1], zero[NS + 1];   // the words this lane loaded: of row lane % 16, group lane / 16 + 4 i
     };
     using Data = std::conditional_t<I4, I4Data, FewData<F>>;
 
-    __device__ __forceinline__ GemvUnits(const GemvArgs &p, int slice, int c0, int c1, const uint8_t *xs, const float *xsum)
-        : p(p), ln(p.K), slice(slice), c0(c0), c1(c1), xs(xs), xsum(xsum), pg(I4 ? p.K / (I4 ? GROUP : 1) : 0),
+    __device__ __forceinline__ GemvUnits(const GemvArgs &p, int slice, int c0, int c1, uint8_t *xs)
+        : p(p), ln(p.K), slice(slice), c0(c0), c1(c1), xs(xs), pg(I4 ? p.K / (I4 ? GROUP : 1) : 0),
           tr(min((int)(threadIdx.x & 15), p.T - 1)) {}
     __device__ __forceinline__ int at(int, int) const { return 0; }
     __device__ __forceinline__ void span(int, int &a, int &b) const {
@@ -191,21 +194,24 @@ struct GemvUnits {
         Operand o;
         o.x = xs + (ln.g * p.T + tr) * 16;
         if constexpr (I4) {
+            constexpr uint32_t half[2] = {0x05040c0cu, 0x07060c0cu};   // of the word, in the upper half of an fp32
+            // one group in a row: an odd one is past its end, and its word may hold another row's scale
+            const uint32_t none = 0x0c0c0c0cu;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const uint32_t at = (uint32_t)gemv_row(p, u, 4 * ln.g + q) * (uint32_t)pg;
-                constexpr uint32_t half[2] = {0x05040c0cu, 0x07060c0cu};   // of the word, in the upper half of an fp32
                 o.even[q] = half[at & 1];
-                // one group in a row: an odd one is past its end, and its word may hold another row's scale
-                o.odd[q] = pg == 1 ? 0x0c0c0c0cu : half[~at & 1];
-                o.zero[q] = 8 * at;
+                o.odd[q] = pg == 1 ? none : half[~at & 1];
             }
+            const uint32_t at = (uint32_t)gemv_row(p, u, ln.r) * (uint32_t)pg + ln.g;
+            o.own = pg == 1 && (ln.g & 1) ? none : half[at & 1];
+            o.zero = 8 * at;
         } else {
             o.lo = (uint32_t)reinterpret_cast<uintptr_t>(p.scales) + (uint32_t)gemv_row(p, u, ln.r) * ln.spitch;
         }
         return o;
     }
-    __device__ __forceinline__ Data fetch(const uint8_t *q, int st, const Operand &o) const {
+    __device__ __forceinline__ Data fetch(const uint8_t *q, int st, int xst, const Operand &o) const {
         Data d;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -214,13 +220,15 @@ struct GemvUnits {
         }
         if constexpr (I4) {
 #pragma unroll
-            for (int j = 0; j < NG; ++j) {
-                d.scale[j] = *reinterpret_cast<const u32x4 *>(q + 2048 + 4 * (16 * j + 4 * ln.g));
-                if constexpr (ZEROS) d.zero[j] = *reinterpret_cast<const u32x4 *>(q + 2048 + 256 * NS + 4 * (16 * j + 4 * ln.g));
-                d.xsum[j] = xsum[((st - c0) * NG + j) * p.T + tr];
+            for (int j = 0; j < NG; ++j) d.scale[j] = *reinterpret_cast<const u32x4 *>(q + 2048 + 4 * (16 * j + 4 * ln.g));
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+                const uint32_t *own = reinterpret_cast<const uint32_t *>(q + 2048 + 256 * i + 4 * (threadIdx.x & 63));
+                d.own[i] = own[0];
+                if constexpr (ZEROS) d.zero[i] = own[64 * NS];
             }
         }
-        const uint8_t *x = o.x + (size_t)(st - c0) * FRAGS * 64 * p.T;
+        const uint8_t *x = o.x + (size_t)(WINDOW ? xst : st - c0) * FRAGS * 64 * p.T;
 #pragma unroll
         for (int f = 0; f < FRAGS; ++f) d.x[f] = *reinterpret_cast<const u32x4 *>(x + f * 64 * p.T);
         return d;
@@ -229,27 +237,51 @@ struct GemvUnits {
         if constexpr (!I4) {
             few_multiply<F>(d, acc);
         } else {
+            // group by group: the sums of (16 + code) x, and of x (the ones' rows are alike)
+            f32x4 part[NG], tokens[NG];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 u32x4 c = d.c[h];
                 few_transpose(c);
-                f32x4 part;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int f = 4 * h + i, j = f * 32 / GROUP;
-                    if (i * 32 % GROUP == 0) part = f32x4{0.f, 0.f, 0.f, 0.f};
-                    part = mfma16x16x32(o.codes.operand(c[i]), d.x[f], part);
-                    if ((i + 1) * 32 % GROUP) continue;
-                    // (past the row the tokens are zero: a scale of this row times zero)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float s = __uint_as_float(__builtin_amdgcn_perm(d.scale[j][e], 0u, j & 1 ? o.odd[e] : o.even[e]));
-                        const float z = ZEROS ? (float)((d.zero[j][e] >> ((o.zero[e] + 8 * (st * NG + j)) & 31)) & 0xFFu) : 8.f;
-                        acc[h][e] = fmaf(s, fmaf(-(16.f + z), d.xsum[j], part[e]), acc[h][e]);
-                    }
+                    if (f * 32 % GROUP == 0) part[j] = tokens[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+                    part[j] = mfma16x16x32(o.codes.operand(c[i]), d.x[f], part[j]);
+                    tokens[j] = mfma16x16x32(u32x4{kOnes, kOnes, kOnes, kOnes}, d.x[f], tokens[j]);
                 }
             }
+            // the groups' offsets, - scale (16 + zero) times the token sums, are an fp32 product over the groups: lane
+            // (r, g) has row r's factor and token r's sum of group g.  (Past the row the tokens are zero and the
+            // scales this row's, or zero.)
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+                const float s = __uint_as_float(__builtin_amdgcn_perm(d.own[i], 0u, o.own));
+                const float z = ZEROS ? (float)((d.zero[i] >> ((o.zero + 8 * (st * NG + 4 * i)) & 31)) & 0xFFu) : 8.f;
+                const bool on = NG > 2 || ln.g < NG;
+                float x = 0.f;
+#pragma unroll
+                for (int j = 0; j < (NG < 4 ? NG : 4); ++j) x = (int)ln.g == j ? tokens[4 * i + j][0] : x;
+                acc[0] = __builtin_amdgcn_mfma_f32_16x16x4f32(on ? -s * (16.f + z) : 0.f, x, acc[0], 0, 0, 0);
+            }
+#pragma unroll
+            for (int j = 0; j < NG; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc[1][e] = fmaf(__uint_as_float(__builtin_amdgcn_perm(d.scale[j][e], 0u, j & 1 ? o.odd[e] : o.even[e])),
+                                     part[j][e], acc[1][e]);
         }
+    }
+    __device__ __forceinline__ uint8_t *tokens(int buffer) const { return xs + (size_t)buffer * WINDOW * FRAGS * 64 * p.T; }
+    __device__ __forceinline__ void stage(int a, int b, int buffer) const {
+        few_request_x<F, kGemvThreads>(p.x, p.ldx, p.T, p.K, a * FRAGS, b * FRAGS, tokens(buffer));
+    }
+    __device__ __forceinline__ void staged(int a, int b, int buffer) const {
+        if constexpr (I4)
+            for (int i = threadIdx.x; i < (b - a) * FRAGS * 4 * p.T; i += kGemvThreads) {
+                u32x4 *v = reinterpret_cast<u32x4 *>(tokens(buffer) + (size_t)i * 16);
+                *v = few_i4_order(*v);
+            }
     }
     __device__ __forceinline__ void finish(int u, int, const f32x4 &sum) const {
         if (p.slices == 1) {
@@ -261,51 +293,24 @@ struct GemvUnits {
     }
 };
 
-// S: steps in each wave's ring.
-template <int F, int GROUP, bool ZEROS, int S>
+// S: steps in each wave's ring.  WINDOW: of the token rows (FewUnits).
+template <int F, int GROUP, bool ZEROS, int S, int WINDOW>
 __global__ __launch_bounds__(kGemvThreads) void gemv_w4_kernel(GemvArgs p) {
     __shared__ GemvSmem sm;
-    using Src = GemvUnits<F, GROUP, ZEROS, S>;
+    using Src = GemvUnits<F, GROUP, ZEROS, S, WINDOW>;
     const int wave = wave_index(), range = blockIdx.x / p.slices, slice = blockIdx.x % p.slices, T = p.T;
     const int nst = few_steps(F, p.K);
     const int c0 = (int)((long long)slice * nst / p.slices), c1 = (int)((long long)(slice + 1) * nst / p.slices);
     const int u0 = (int)((long long)range * p.units / p.ranges), u1 = (int)((long long)(range + 1) * p.units / p.ranges);
-    uint8_t *xs = sm.area + kGemvWaves * S * Src::SLOT;
-    const int nx = (c1 - c0) * Src::FRAGS * 4 * T;   // 16-byte pieces of the token rows
-    [[maybe_unused]] float *xsum = reinterpret_cast<float *>(xs + (size_t)nx * 16);
-    const Src src(p, slice, c0, c1, xs, xsum);
+    const Src src(p, slice, c0, c1, sm.area + kGemvWaves * S * Src::SLOT);
     FewUnits<Src> run(src, sm.area, sm.red);
-
-    // token rows of this K range, zero past K: requested before the weights, so that they arrive first
-    [[maybe_unused]] const size_t xbytes = (size_t)((T - 1) * p.ldx + p.K) * 2;
-    for (int i = threadIdx.x; i < nx; i += kGemvThreads) {
-        const int t = i % T, fg = i / T, k = few_frag_k<F>(c0 * Src::FRAGS + (fg >> 2), fg & 3);
-        if (k < p.K)
-            dma16<false>(MOE_CHECKED(p.x + t * p.ldx + k, 16, p.x, xbytes), xs + (size_t)(i - (threadIdx.x & 63)) * 16);
-        else
-            *reinterpret_cast<u32x4 *>(xs + (size_t)i * 16) = u32x4{0u, 0u, 0u, 0u};
-    }
+    // the token rows are requested before the weights, so that they arrive first
+    if constexpr (WINDOW == 0) src.stage(c0, c1, 0);
     run.start(u0, u1, 0, c1 - c0);
-    if (run.more()) few_wait<S * Src::OPS>();   // the ring's S steps are behind them
-    else few_wait<0>();
-    if constexpr (F == kFewI4)
-        for (int i = threadIdx.x; i < nx; i += kGemvThreads) {
-            u32x4 *v = reinterpret_cast<u32x4 *>(xs + (size_t)i * 16);
-            *v = few_i4_order(*v);
-        }
-    __syncthreads();
-    if constexpr (F == kFewI4) {
-        constexpr int per = GROUP / 8;   // 16-byte pieces of one group and token, at stride 16 T
-        for (int i = threadIdx.x; i < nx / per; i += kGemvThreads) {
-            const int t = i % T, grp = i / T;
-            float s = 0.f;
-            for (int j = 0; j < per; ++j) {
-                const u32x4 v = *reinterpret_cast<const u32x4 *>(xs + ((size_t)(grp * per + j) * T + t) * 16);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) s += bf16_to_f32(v[q] & 0xFFFFu) + bf16_to_f32(v[q] >> 16);
-            }
-            xsum[i] = s;
-        }
+    if constexpr (WINDOW == 0) {
+        if (run.more()) few_wait<S * Src::OPS>();   // the ring's S steps are behind them
+        else few_wait<0>();
+        src.staged(c0, c1, 0);
         __syncthreads();
     }
     run.run();
@@ -333,37 +338,37 @@ __global__ __launch_bounds__(kGemvThreads) void gemv_w4_kernel(GemvArgs p) {
     }
 }
 
-// Steps in a ring: the deepest that leaves the token rows room.
-constexpr int kGemvDeep = 6, kGemvMiddle = 4, kGemvShallow = 3;
-
-// LDS bytes that `steps` steps of token rows (and INT4's token sums) take.
-size_t gemv_x_bytes(int T, int steps) { return (size_t)steps * 512 * T + (size_t)steps * 32 * T; }
-size_t gemv_ring_bytes(int slot, int s) { return (size_t)kGemvWaves * s * slot; }
+// Steps in a ring: the deepest that leaves the whole token rows room, else the
+// one that leaves room for windows of four steps.
+constexpr int kGemvDeep = 6, kGemvMiddle = 4, kGemvShallow = 3, kGemvWindow = 4;
 
 template <int F, int GROUP, bool ZEROS>
 void launch_format(const GemvArgs &p, hipStream_t st) {
     constexpr int slot = GemvSlot<F, GROUP, ZEROS>::SLOT;
+    constexpr int windows = 2 * kGemvWindow * FewStep<F>::FRAGS * 64 * kFewTokens;
+    constexpr int S = (kGemvArea - windows) / (kGemvWaves * slot);
+    static_assert(S >= 3, "a ring next to the windows");
     const dim3 grid(p.ranges * p.slices), block(kGemvThreads);
-    const int steps = (few_steps(F, p.K) + p.slices - 1) / p.slices;
-    auto fits = [&](int s) { return gemv_x_bytes(p.T, steps) + gemv_ring_bytes(slot, s) <= (size_t)kGemvArea; };
-    if (fits(kGemvDeep)) gemv_w4_kernel<F, GROUP, ZEROS, kGemvDeep><<<grid, block, 0, st>>>(p);
-    else if (fits(kGemvMiddle)) gemv_w4_kernel<F, GROUP, ZEROS, kGemvMiddle><<<grid, block, 0, st>>>(p);
-    else gemv_w4_kernel<F, GROUP, ZEROS, kGemvShallow><<<grid, block, 0, st>>>(p);
+    const long long x = (long long)(few_steps(F, p.K) + p.slices - 1) / p.slices * FewStep<F>::FRAGS * 64 * p.T;
+    auto fits = [&](int s) { return x + kGemvWaves * s * slot <= kGemvArea; };
+    if (fits(kGemvDeep)) gemv_w4_kernel<F, GROUP, ZEROS, kGemvDeep, 0><<<grid, block, 0, st>>>(p);
+    else if (fits(kGemvMiddle)) gemv_w4_kernel<F, GROUP, ZEROS, kGemvMiddle, 0><<<grid, block, 0, st>>>(p);
+    else if (fits(kGemvShallow)) gemv_w4_kernel<F, GROUP, ZEROS, kGemvShallow, 0><<<grid, block, 0, st>>>(p);
+    else gemv_w4_kernel<F, GROUP, ZEROS, S, kGemvWindow><<<grid, block, 0, st>>>(p);
 }
 
 }  // namespace
 
-// Workgroups of a product: `ranges` of units times `slices` of K, as many
-// slices as the token rows need to fit the LDS next to the shallow ring.
-GemvPlan gemv_plan(GemvFormat fmt, int group, bool zeros, int T, int N, int K, bool geglu) {
+// Workgroups of a product: `ranges` of units times `slices` of K, several
+// slices where there are few units and a long K (sixteen steps or more to a
+// slice, two for each of its waves).
+GemvPlan gemv_plan(int N, int K, bool geglu) {
     GemvPlan g;
     g.outs = geglu ? N / 2 : N;
     g.units = geglu ? (g.outs + 7) / 8 : (N - 1) / 16 + 1;
     const int steps = (K - 1) / 256 + 1;
-    const int words = fmt == GemvFormat::kINT4 ? (group == 32 ? 2 : 1) * (zeros ? 2 : 1) : fmt == GemvFormat::kNVFP4 ? 2 : 1;
-    const int fit = (int)((kGemvArea - gemv_ring_bytes(2048 + 256 * words, kGemvShallow)) / gemv_x_bytes(T, 1));
-    g.slices = (steps + fit - 1) / fit;
-    g.ranges = std::min(g.units, std::max(1, kGemvBlocks / g.slices));
+    g.slices = std::max(1, std::min(kGemvBlocks / g.units, steps / 16));
+    g.ranges = std::min(g.units, kGemvBlocks / g.slices);
     return g;
 }
 
@@ -372,7 +377,7 @@ size_t gemv_part_bytes(const GemvPlan &g, int T) {
 }
 
 hipError_t launch_gemv_w4(const GemvW4 &l, hipStream_t st) {
-    const GemvPlan g = gemv_plan(l.fmt, l.group, l.zeros != nullptr, l.T, l.N, l.K, l.geglu);
+    const GemvPlan g = gemv_plan(l.N, l.K, l.geglu);
     GemvArgs p{};
     p.x = l.x;
     p.w = l.w;

@@ -102,13 +102,14 @@ def test_gemv_arguments(lib):
     assert gemv(lib, W(f=3, group=0), scales=MIS) == -1
     assert gemv(lib, W(), scales=MIS) == -1 and gemv(lib, W(), zeros=MIS) == -1 and gemv(lib, W(f=1, group=0), scales=MIS) == -1
     assert gemv(lib, W(f=1, group=0), zeros=F) == -1 and gemv(lib, W(f=3, group=0), zeros=F) == -1
-    # token rows too long for one workgroup: partial sums, so a workspace
+    # few rows and a long K: partial sums, so a workspace
     s = W(T=16, K=1 << 16)
     need = lib.moe_gemv_w4_workspace_bytes(ctypes.byref(s))
     assert need > moe.FEW_ZERO_BYTES
     assert gemv(lib, s, ws=None) == -3 and gemv(lib, s, n=need - 1) == -3 and gemv(lib, s, ws=F + 4) == -3
-    # the largest K there is still has a counter per range
-    assert lib.moe_gemv_w4_workspace_bytes(ctypes.byref(W(T=16, N=1 << 20, K=1 << 20))) > 0
+    # many rows, or a short K: none
+    assert lib.moe_gemv_w4_workspace_bytes(ctypes.byref(W(T=16, N=1 << 20, K=1 << 20))) == 0
+    assert lib.moe_gemv_w4_workspace_bytes(ctypes.byref(W(T=16, K=4096))) == 0
 
 
 def test_binding_refusals():
