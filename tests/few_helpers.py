@@ -5,8 +5,9 @@ the arithmetic.
 Bounds.  A sum of K fp32 products on the matrix cores is off by at most
 (K/32 + 32) 2^-24 times the sum of the products' magnitudes (one rounding per
 32-wide step and at most 32 inside one; products of bf16 values are exact);
-the later fp32 additions (waves, experts, slices: at most 64 of them, bias)
-add 2^-24 of the running magnitude each.  Rounding to bf16 is off by at most
+the later fp32 additions (waves, slices: at most 64 of them, experts in at most
+sixteen segments each, bias) add 2^-24 of the running magnitude each.  INT4
+groups are added one by one, their sums and their offsets: K/32 more.    Rounding to bf16 is off by at most
 2^-8 of the value.  gelu_tanh has slope at most 1.13 and is evaluated to
 within 2^-19 of |z| (exp of an argument of magnitude up to 88 carries that
 argument's rounding, 88 * 2^-24 < 2^-17.5, only where the result is below
@@ -138,7 +139,7 @@ class Layer:
                 mlp(t, w[t, j], self.gu.values[ids[t, j]], self.d.values[ids[t, j]], self.I)
             if self.I_sh:
                 mlp(t, 1.0, self.sgu.values[0], self.sd.values[0], self.I_sh)
-        err = err + 64 * U * mag
+        err = err + (64 + 16 * k) * U * mag
         return out, err + BF * (np.abs(out) + err) + 2.0 ** -133, ids, w
 
     def check(self, got, label=""):
@@ -205,7 +206,8 @@ class Gemv:
 
     def reference(self):
         x = f64(self.x)[:, :self.K]
-        c = (self.K / 32 + 32 + 300) * U           # 256 slices, eight waves, the bias
+        # 256 slices, eight waves, the bias
+        c = (self.K / (16 if self.fmt == "int4" else 32) + 32 + 300) * U
         y, m = x @ self.values.T, np.abs(x) @ self.mags.T
         if self.bias is not None:
             y, m = y + f64(self.bias), m + np.abs(f64(self.bias))

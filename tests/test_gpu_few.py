@@ -30,6 +30,11 @@ SHAPES = {
     "mlp-shorter": dict(T=16, H=192, E=16, k=4, I=256, I_sh=64),
     "long-rows": dict(T=16, H=4160, E=4, k=2, I=64),
     "long-rows-one": dict(T=1, H=8256, E=3, k=1, I=64, I_sh=64),
+    "long-rows-many-units": dict(T=16, H=3264, E=9, k=9, I=2112, I_sh=192),
+    "pieces": dict(T=16, H=128, E=4, k=2, I=1600, I_sh=1984),
+    "pieces-of-column-blocks": dict(T=8, H=64, E=12, k=2, I=2112, I_sh=704),
+    "passes": dict(T=16, H=64, E=32, k=32, I=6400),
+    "fewest-items": dict(T=16, H=64, E=2, k=2, I=64),
 }
 
 
@@ -52,6 +57,14 @@ def test_model_width(gpu, fmt):
     """The model's rows (2816, 704, dense 2112) with fewer experts."""
     l = Layer(8, 2816, 10, 4, 704, I_sh=2112, fmt=fmt)
     l.check(l.run(), f"model width {fmt}")
+
+
+@pytest.mark.parametrize("T,H", [(t, h) for t in (3, 6, 11, 16) for h in (512, 2048, 2816, 5120)])
+@pytest.mark.parametrize("fmt", FMTS)
+def test_every_ring(gpu, fmt, T, H):
+    """Token rows that leave the rings less and less of the LDS, then none."""
+    l = Layer(T, H, 4, 2, 128, fmt=fmt, seed=H)
+    l.check(l.run(), f"T={T} H={H} {fmt}")
 
 
 @pytest.mark.parametrize("T", [1, 4, 16])

@@ -10,7 +10,7 @@ from few_helpers import Gemv, f64
 pytestmark = pytest.mark.gpu
 
 FORMATS = [("mxfp4", 0), ("nvfp4", 0), ("int4", 32), ("int4", 64), ("int4", 128)]
-SIZES = [(1, 1, 128), (1, 16, 256), (3, 17, 384), (16, 250, 640), (5, 33, 2816), (2, 1000, 128), (8, 8, 1152),
+SIZES = [(16, 40, 8192), (16, 9000, 384), (4, 70, 33024), (1, 1, 128), (1, 16, 256), (3, 17, 384), (16, 250, 640), (5, 33, 2816), (2, 1000, 128), (8, 8, 1152),
          (1, 5000, 256), (16, 31, 16384), (7, 2, 4096)]
 
 
@@ -126,6 +126,37 @@ def test_overlapping_calls(gpu):
     torch.cuda.synchronize()
     for o, r in zip(outs, refs):
         assert all(torch.equal(y, r) for y in o)
+
+
+@pytest.mark.parametrize("fmt,group", [("mxfp4", 0), ("int4", 64)])
+def test_long_rows_in_several_rounds(gpu, fmt, group):
+    """Token rows that come to the LDS in windows, several rounds of units for
+    each workgroup: the first, some middle and the last rows."""
+    T, N, K = 16, 35_003, 5504
+    gen = torch.Generator().manual_seed(7)
+    codes = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device="cuda")
+    x = torch.randn(T, K, generator=gen).to(torch.bfloat16)
+    if fmt == "int4":
+        scales = torch.rand(N, K // group, generator=gen).to(torch.bfloat16)
+    else:
+        scales = torch.randint(118, 124, (N, K // 32), generator=gen, dtype=torch.uint8)
+    y = torch.empty(T, N, dtype=torch.float32, device="cuda")
+    s = moe.w4_shape(T, N, K, fmt, group=group, y_fp32=True)
+    moe.gemv_w4(s, x.cuda(), codes, scales.cuda(), None, None, y, dev.gemv_workspace(s))
+    torch.cuda.synchronize()
+    lut = torch.tensor([0, .5, 1, 1.5, 2, 3, 4, 6, 0, -.5, -1, -1.5, -2, -3, -4, -6], dtype=torch.float64)
+    for at in (0, 12_345, N - 64):
+        c = codes[at:at + 64].cpu().long()
+        c = torch.stack((c & 15, c >> 4), -1).reshape(64, K)
+        if fmt == "int4":
+            sc = scales[at:at + 64].double().repeat_interleave(group, 1)
+            w, mag, n = sc * (c - 8), sc * (15 + 8 + 32), K / 16
+        else:
+            w = lut[c] * 2.0 ** (scales[at:at + 64].double().repeat_interleave(32, 1) - 127)
+            mag, n = w.abs(), K / 32
+        xd = x.double()
+        bound = (n + 332) * 2.0 ** -24 * (xd.abs() @ mag.T)
+        assert ((y[:, at:at + 64].cpu().double() - xd @ w.T).abs() <= bound).all()
 
 
 def test_many_rows(gpu):
