@@ -330,6 +330,8 @@ int moe_quantize_nv(const uint16_t *src, int64_t rows, int32_t K, const float *i
 
 /* Largest token count of moe_forward_few and moe_gemv_w4. */
 #define MOE_FEW_MAX_TOKENS 16
+/* Largest H, I and I_sh of moe_forward_few. */
+#define MOE_FEW_MAX_WIDTH 65536
 /* Leading workspace bytes of moe_forward_few and moe_gemv_w4 that must start
  * out zero. */
 #define MOE_FEW_ZERO_BYTES 4096
@@ -347,7 +349,8 @@ int moe_quantize_nv(const uint16_t *src, int64_t rows, int32_t K, const float *i
  *                    MOE_W_BF16, MOE_W_MXFP4 and MOE_W_NVFP4 (the dense MLP
  *                    in the experts' format too, an NVFP4 one with a scale
  *                    buffer for E = 1); 4-bit codes 16-byte, scales 4-byte
- *                    aligned
+ *                    aligned and read in whole 4-byte words: up to 3 bytes
+ *                    behind the last value, in the same word, are read too
  *   I_sh             0 (no dense MLP: its four arguments are ignored) or a
  *                    positive multiple of 64
  *   out              [T][H] bf16 out, no overlap with the inputs
@@ -359,7 +362,8 @@ int moe_quantize_nv(const uint16_t *src, int64_t rows, int32_t K, const float *i
  *                    calls (of moe_gemv_w4 too) that do not overlap in time.
  *                    With other contents the results are undefined (the
  *                    kernel still ends).
- * MOE_ERR_UNSUPPORTED for T above the limit and the W4A4 formats.  Non-finite
+ * MOE_ERR_UNSUPPORTED for T, H, I or I_sh above the limits and the W4A4
+ * formats.  Non-finite
  * values in a token's x affect that token's output only.
  */
 int moe_forward_few(const moe_shape *s, const uint16_t *x, const uint16_t *w_router,
@@ -404,12 +408,13 @@ enum {
  *           bytes behind the last value, in the same word, are read too)
  *   bias    [N] fp32 or NULL
  *   y       [T][ldy] out (N, or N/2 columns with GEGLU), bf16 (2-byte
- *           aligned) or fp32 (4-byte aligned); what lies between the rows is
- *           not written
+ *           aligned) or fp32 (4-byte aligned), no overlap with the inputs;
+ *           what lies between the rows is not written
  *   ws      device scratch of at least moe_gemv_w4_workspace_bytes(s), with
  *           the zero-prefix rule of moe_forward_few; may be NULL when that is 0
  * A non-finite value in a row of x makes that row's outputs non-finite
- * (INT4: NaN) and affects no other row.  The same call gives the same bits.
+ * (INT4: NaN) and affects no other row; a scale that is not finite makes its
+ * weight row's outputs non-finite.  The same call gives the same bits.
  */
 int moe_gemv_w4(const moe_w4_shape *s, const uint16_t *x, const uint8_t *w, const uint8_t *scales,
                 const uint8_t *zeros, const float *bias, void *y, void *ws, size_t ws_bytes,

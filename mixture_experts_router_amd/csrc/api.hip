@@ -186,6 +186,8 @@ int check_few(const moe_shape *s, int32_t I_sh) {
     if (st != MOE_OK) return st;
     if (I_sh < 0) return MOE_ERR_INVALID_ARGUMENT;
     if (s->T > MOE_FEW_MAX_TOKENS || I_sh % 64 != 0) return MOE_ERR_UNSUPPORTED;
+    // (the kernel counts units, segments of rows and values of out in 32 bits)
+    if (s->H > MOE_FEW_MAX_WIDTH || s->I > MOE_FEW_MAX_WIDTH || I_sh > MOE_FEW_MAX_WIDTH) return MOE_ERR_UNSUPPORTED;
     if (s->w_format == MOE_W_MXFP4_A4 || s->w_format == MOE_W_NVFP4_A4) return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }
@@ -607,7 +609,7 @@ int moe_forward_few(const moe_shape *s, const uint16_t *x, const uint16_t *w_rou
 
 size_t moe_gemv_w4_workspace_bytes(const moe_w4_shape *s) {
     if (check_w4(s) != MOE_OK) return 0;
-    const size_t part = moe::gemv_part_bytes(moe::gemv_plan(s->N, s->K, s->flags & MOE_GEMV_GEGLU), s->T);
+    const size_t part = moe::gemv_part_bytes(moe::gemv_plan(s->T, s->N, s->K, s->flags & MOE_GEMV_GEGLU), s->T);
     return part ? MOE_FEW_ZERO_BYTES + round_up(part) : 0;
 }
 

@@ -3,7 +3,7 @@
 // With few tokens the layer is a stream of expert weights: each touched
 // expert's gate/up and down matrices are read once and multiplied with every
 // token (few_stream.h), so the bytes bound it and launches and waits are the
-// rest of its time.  One persistent grid runs three phases:
+// rest of its time.  One persistent grid runs the phases:
 //
 //   router   logits = x W_r^T (+ b), four experts per work item, summed as
 //            moe_route does (fp32 chunks of 256, added in fp64), so both give
@@ -11,15 +11,32 @@
 //   gate/up  every workgroup selects the experts itself (top-k of the few
 //            tokens from the logits), then h = gelu_tanh(g) * u for its share
 //            of the (expert, 8 columns) units, rounded to bf16
-//   down     out[t][16 columns] = sum over experts of w[t, e] * (W_d h): the
-//            routing weights multiply the fp32 sums, experts are added in a
-//            fixed order, and out is rounded once
+//   down     y[t, e][16 columns] = W_d h in fp32, the units of all touched
+//            experts shared evenly; with up to 16 assignments instead
+//            out[t][16 columns] = sum over experts of w[t, e] * (W_d h)
+//   combine  (where down stored y) out = sum over experts of w[t, e] * y: the
+//            routing weights multiply fp32 sums, experts are added in a fixed
+//            order, and out is rounded once
 //
 // Each phase's items are handed out by a ticket counter.  A workgroup takes
-// router items while there are any, then gate/up shares, then down items, and
-// waits only for items of an earlier phase, all of which have then been taken
-// by workgroups that are running: every wait ends, whatever else runs on the
-// GPU and however few workgroups are resident.
+// router items while there are any, then gate/up shares, then down items, then
+// combine items, and waits only for items of an earlier phase, all of which
+// have then been taken by workgroups that are running: every wait ends,
+// whatever else runs on the GPU and however few workgroups are resident.
+//
+// h is rounded to bf16, the operand type of the down product's MFMAs; nothing
+// else is rounded below fp32 before out.
+//
+// Measured at hidden 2816, 128 experts, top-8, expert intermediate 704, one
+// call after another: 1 token 36.7 us in bf16 (95.9 MB of weights) and 28.2
+// in MXFP4 (26.0 MB), 8 tokens 118 (615 MB: 5.2 TB/s) and 62 (164 MB), 5
+// tokens in NVFP4 55 (119 MB), 16 tokens with the dense MLP in bf16 183
+// (1.02 GB: 5.6 TB/s).  Of the 8 bf16 tokens' time 13 us pass before the first
+// expert weight is requested (start 2, ticket and router 5, top-k 6), 58 in
+// gate/up (7.0 TB/s), 9 until h has arrived everywhere, 28 in down (7.3 TB/s,
+// first weights requested before h is there), 6 in combine.  What bounds it:
+// the bytes, and with one token the chain of dependent trips to memory between
+// the phases.
 #include <algorithm>
 
 #include "few_stream.h"
@@ -32,7 +49,7 @@ namespace {
 
 constexpr int kFewWaves = 8, kFewThreads = 64 * kFewWaves;
 constexpr int kFewMaxA = kFewTokens * 32;                 // assignments (k <= 32)
-constexpr int kFewArea = 136 * 1024;                      // LDS for the rings and the token rows
+constexpr int kFewArea = 136 * 1024;                      // LDS for the rings and the token rows (the rest: 23 KB)
 
 // Counters in the workspace's zeroed prefix, a line each: tickets (the next
 // item of each phase), items done, workgroups left.  A phase's items done are
@@ -685,7 +702,12 @@ __global__ __launch_bounds__(kFewThreads) void few_layer_kernel(FewArgs p) {
 }
 
 // Steps in a ring: the deepest that leaves the token rows room (bf16 or 4-bit,
-// by slot size), else the one that leaves room for windows of them.
+// by slot size), else the one that leaves room for windows of them.  A short
+// ring next to whole rows is better than a deep one next to windows, which cost
+// a barrier each and leave the last units unsplit: 16 tokens, hidden 2816, bf16
+// with MLP 183 us (3 steps) against 190 (6 steps); 12 tokens, hidden 4096,
+// NVFP4 74 (2) against 83 (4).  Windows against rows read from global memory, 16
+// tokens, hidden 5120: bf16 178 us against 230, MXFP4 95 against 153.
 constexpr int kRings = 3, kRing[2][kRings + 1] = {{7, 5, 3, 6}, {6, 4, 2, 4}}, kWindow[2] = {8, 4};
 
 struct FewPlan {
@@ -708,6 +730,9 @@ FewPlan few_plan(int f, int T, int H, int k, int I, int I_sh) {
     g.PW = (st + want - 1) / want;
     g.ne = (st + g.PW - 1) / g.PW;
     g.ns = (few_steps(f, I_sh) + g.PW - 1) / g.PW;
+    // Column blocks need all rows of h in every workgroup and use H / 16 of them, but no combine phase: hidden
+    // 2816, top-8, one token 36.8 us in bf16 and 28.4 in MXFP4 against 41.4 and 32.5 with shared units, two tokens
+    // 49.9 and 37.3 against 51.4 and 38.8; three tokens 66.1 and 42.4 against 63.7 and 39.5.
     g.columns = T * k <= 16;
     g.y = g.columns ? 0 : ((size_t)T * k * g.ne + (size_t)T * g.ns) * H;
     return g;

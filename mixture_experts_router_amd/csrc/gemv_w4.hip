@@ -4,11 +4,19 @@
 //
 // A weight is read once and multiplied with every token (few_stream.h), so
 // the weight bytes bound the product.  A workgroup keeps the token rows of its
-// K range in LDS in MFMA order and runs through a range of 16-row units; a
-// unit's K is split over as many of its waves as the range leaves free.  Sums
-// are fp32 and rounded once.  Where the token rows of the whole K exceed the
-// LDS, several workgroups share a range along K: each stores its fp32 sums,
-// and the last to finish adds them in K order, whichever it is.
+// K range in LDS in MFMA order (or windows of them, where they do not fit) and
+// runs through a range of 16-row units.  Sums are fp32 and rounded once.  Where
+// there are few units and a long K, several workgroups share a range along K:
+// each stores its fp32 sums, and the last to finish adds them in K order,
+// whichever it is.
+//
+// Measured: 1 token x 2112 -> 2816 in INT4 and x 2816 -> 2112 GEGLU in MXFP4 6.3
+// us, which is the host's time for a call (7.5 and 5.8 on the GPU under the
+// profiler); 8 tokens x 2816 -> 5001 INT4 9.2; 4 tokens x 8192 -> 8192 NVFP4
+// 13.1 (37.9 MB: 2.9 TB/s), 10.8 without its arithmetic; 16 tokens x 2816 ->
+// 131072 INT4 58 (205 MB: 3.5 TB/s).  The last is bound by its instructions,
+// 160 vector and 17 matrix ones to a step of 16 x 256 weights, and by the three
+// steps of a ring that 90 KB of token rows leave room for.
 //
 // INT4: W = scale (code - zero) with one scale and zero per group of 32, 64 or
 // 128 K values.  The matrix cores multiply the exact values 16 + code, one
@@ -339,7 +347,9 @@ __global__ __launch_bounds__(kGemvThreads) void gemv_w4_kernel(GemvArgs p) {
 }
 
 // Steps in a ring: the deepest that leaves the whole token rows room, else the
-// one that leaves room for windows of four steps.
+// one that leaves room for windows of four steps (which cost barriers: 16
+// tokens x 2816 -> 131072 in INT4 58 us with whole rows and three steps, 72
+// with windows and four).
 constexpr int kGemvDeep = 6, kGemvMiddle = 4, kGemvShallow = 3, kGemvWindow = 4;
 
 template <int F, int GROUP, bool ZEROS>
@@ -360,14 +370,15 @@ void launch_format(const GemvArgs &p, hipStream_t st) {
 }  // namespace
 
 // Workgroups of a product: `ranges` of units times `slices` of K, several
-// slices where there are few units and a long K (sixteen steps or more to a
-// slice, two for each of its waves).
-GemvPlan gemv_plan(int N, int K, bool geglu) {
+// slices where the token rows do not fit the LDS (next to a shallow ring) and
+// there are too few units for all workgroups.
+GemvPlan gemv_plan(int T, int N, int K, bool geglu) {
     GemvPlan g;
     g.outs = geglu ? N / 2 : N;
     g.units = geglu ? (g.outs + 7) / 8 : (N - 1) / 16 + 1;
-    const int steps = (K - 1) / 256 + 1;
-    g.slices = std::max(1, std::min(kGemvBlocks / g.units, steps / 16));
+    const int steps = (K - 1) / 256 + 1, fit = (kGemvArea - kGemvWaves * kGemvShallow * 2304) / (512 * T);
+    // (to no fewer than 16 steps, two for each wave, beyond what the LDS asks for)
+    g.slices = steps <= fit ? 1 : std::max(1, std::min(kGemvBlocks / g.units, std::max((steps + fit - 1) / fit, steps / 16)));
     g.ranges = std::min(g.units, kGemvBlocks / g.slices);
     return g;
 }
@@ -377,7 +388,7 @@ size_t gemv_part_bytes(const GemvPlan &g, int T) {
 }
 
 hipError_t launch_gemv_w4(const GemvW4 &l, hipStream_t st) {
-    const GemvPlan g = gemv_plan(l.N, l.K, l.geglu);
+    const GemvPlan g = gemv_plan(l.T, l.N, l.K, l.geglu);
     GemvArgs p{};
     p.x = l.x;
     p.w = l.w;

@@ -134,7 +134,7 @@ enum class GemvFormat { kMXFP4, kNVFP4, kINT4 };
 struct GemvPlan {
     int outs, units, ranges, slices;
 };
-GemvPlan gemv_plan(int N, int K, bool geglu);
+GemvPlan gemv_plan(int T, int N, int K, bool geglu);
 size_t gemv_part_bytes(const GemvPlan &g, int T);   // 0: no workspace needed
 struct GemvW4 {
     const uint16_t *x;

@@ -51,7 +51,7 @@ def test_header_constants():
 @pytest.mark.parametrize("s,expect", [
     (None, -1), (S(T=0), -1), (S(H=0), -1), (S(E=0), -1), (S(k=0), -1), (S(I=0), -1), (S(k=9), -1), (S(T=17), -2),
     (S(T=1 << 20), -2), (S(H=96), -2), (S(I=100), -2), (S(E=2000), -2), (S(E=64, k=33), -2), (S(f=2), -2),
-    (S(f=4), -2), (S(f=5), -2), (S(f=-1), -2),
+    (S(f=4), -2), (S(f=5), -2), (S(f=-1), -2), (S(H=65600), -2), (S(I=65600), -2), (S(H=1 << 28), -2),
 ])
 def test_few_shapes(lib, s, expect):
     assert few(lib, s, gus=F, ds=F) == expect
@@ -70,7 +70,7 @@ def test_few_arguments(lib):
     assert few(lib, S(f=1), gus=MIS, ds=F) == -1                          # scales 4-byte aligned
     assert few(lib, S(f=3), gus=F, ds=MIS) == -1                          # NVFP4 scale buffers 4-byte aligned
     assert few(lib, S(), I_sh=-64) == -1
-    assert few(lib, S(), I_sh=100, sgu=F, sd=F) == -2
+    assert few(lib, S(), I_sh=100, sgu=F, sd=F) == -2 and few(lib, S(), I_sh=65600, sgu=F, sd=F) == -2
     assert few(lib, S(), I_sh=128, sgu=F) == -1
     assert few(lib, S(), I_sh=128, sgu=F, sd=F, sds=F) == -1
     assert few(lib, S(f=3), gus=F, ds=F, I_sh=128, sgu=F, sd=F, sgus=F) == -1
@@ -109,7 +109,8 @@ def test_gemv_arguments(lib):
     assert gemv(lib, s, ws=None) == -3 and gemv(lib, s, n=need - 1) == -3 and gemv(lib, s, ws=F + 4) == -3
     # many rows, or a short K: none
     assert lib.moe_gemv_w4_workspace_bytes(ctypes.byref(W(T=16, N=1 << 20, K=1 << 20))) == 0
-    assert lib.moe_gemv_w4_workspace_bytes(ctypes.byref(W(T=16, K=4096))) == 0
+    assert lib.moe_gemv_w4_workspace_bytes(ctypes.byref(W(T=16, K=2816))) == 0
+    assert lib.moe_gemv_w4_workspace_bytes(ctypes.byref(W(T=1, K=16384))) == 0
 
 
 def test_binding_refusals():
