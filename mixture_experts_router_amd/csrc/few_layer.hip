@@ -415,7 +415,7 @@ __device__ __forceinline__ void few_gateup(const FewArgs &p, FewSmem &sm, bool s
 
 // ---------------------------------------------------------------- down
 // The K of the down products comes in segments: an expert's row, or pieces of
-// it where sixteen rows of h would not fit the LDS, then the dense MLP in
+// it where T rows of h would not fit the LDS, then the dense MLP in
 // pieces of the same size.  Units of sixteen output columns of one segment.
 //
 // COLUMNS: an item is one block of columns, all segments, added in registers
@@ -426,9 +426,15 @@ __device__ __forceinline__ void few_gateup(const FewArgs &p, FewSmem &sm, bool s
 // h is staged in LDS for as many segments as fit (a pass); the ring's first
 // weights of a pass are requested before its h is staged, those of the first
 // one before h exists.
-template <int F, int S_, bool COLUMNS>
+//
+// The token rows of gate/up are gone by then, so the rings need not be theirs:
+// 8 tokens in MXFP4 take 61.6 us with six steps, 63.7 with three; in bf16 three
+// are enough (117.9 with seven, 118.1), 16 tokens with MLP 186.4 with seven, 183.3.
+constexpr int few_down_ring(int f) { return f == kFewBf16 ? 3 : 6; }
+
+template <int F, bool COLUMNS>
 struct FewDown {
-    static constexpr int S = S_, SLOT = FewStep<F>::SLOT, OPS = FewStep<F>::OPS, WINDOW = 0;
+    static constexpr int S = few_down_ring(F), SLOT = FewStep<F>::SLOT, OPS = FewStep<F>::OPS, WINDOW = 0;
     using Rows = FewRows;
     using Operand = FewOperand<F>;
     static constexpr int KS = FewStep<F>::K;
@@ -543,9 +549,9 @@ struct FewDown {
     }
 };
 
-template <int F, int S, bool COLUMNS>
+template <int F, bool COLUMNS>
 __device__ __forceinline__ void few_down_items(const FewArgs &p, FewSmem &sm, int item) {
-    using Src = FewDown<F, S, COLUMNS>;
+    using Src = FewDown<F, COLUMNS>;
     const int lane = threadIdx.x & 63, wave = wave_index();
     Src src(p, sm);
     FewUnits<Src> run(src, sm.area, sm.red);
@@ -572,8 +578,9 @@ __device__ __forceinline__ void few_down_items(const FewArgs &p, FewSmem &sm, in
             run.start(u, ub, va, src.PW);
             if (u == u0) {
                 if (threadIdx.x == 0) {
+                    const uint32_t n = ctr_ticket(p, kDown);   // (on its way while this waits)
                     if (!have_h) wait_done(p, kGateUp);
-                    sm.down = (int)ctr_ticket(p, kDown);
+                    sm.down = (int)n;
                 }
                 __syncthreads();
                 next = uniform(sm.down);
@@ -676,8 +683,8 @@ __global__ __launch_bounds__(kFewThreads) void few_layer_kernel(FewArgs p) {
         if ((uint32_t)t >= (uint32_t)p.n_gu) break;
     }
     if ((uint32_t)d < (uint32_t)p.n_down) {
-        if (p.columns) few_down_items<F, S, true>(p, sm, d);
-        else few_down_items<F, S, false>(p, sm, d);
+        if (p.columns) few_down_items<F, true>(p, sm, d);
+        else few_down_items<F, false>(p, sm, d);
     }
     if (!p.columns) {
         int c = 0;
@@ -726,7 +733,7 @@ FewPlan few_plan(int f, int T, int H, int k, int I, int I_sh) {
     auto rest = [&](int i) { return kFewArea - kFewWaves * rings[i] * few_slot(f); };
     while (g.ring < kRings && (long long)few_steps(f, H) * step * T > rest(g.ring)) ++g.ring;
     // segments of which T rows of h fit
-    const int most = (rest(g.ring) / T - 16) / step, st = few_steps(f, I), want = (st + most - 1) / most;
+    const int most = ((kFewArea - kFewWaves * few_down_ring(f) * few_slot(f)) / T - 16) / step, st = few_steps(f, I), want = (st + most - 1) / most;
     g.PW = (st + want - 1) / want;
     g.ne = (st + g.PW - 1) / g.PW;
     g.ns = (few_steps(f, I_sh) + g.PW - 1) / g.PW;
@@ -742,7 +749,7 @@ template <int F, int R = 0>
 void launch_format(const FewArgs &p, int ring, int blocks, hipStream_t st) {
     constexpr int S = kRing[F != kFewBf16][R], W = R == kRings ? kWindow[F != kFewBf16] : 0;
     static_assert(2 * W * FewStep<F>::FRAGS * 64 * kFewTokens <= kFewArea - kFewWaves * S * FewStep<F>::SLOT, "windows");
-    static_assert((kFewArea - kFewWaves * S * FewStep<F>::SLOT) / kFewTokens >= 16 + FewStep<F>::K * 2,
+    static_assert((kFewArea - kFewWaves * few_down_ring(F) * FewStep<F>::SLOT) / kFewTokens >= 16 + FewStep<F>::K * 2,
                   "a segment is one step or more");
     if (ring == R) {
         few_layer_kernel<F, S, W><<<blocks, kFewThreads, 0, st>>>(p);
