@@ -340,9 +340,10 @@ int moe_quantize_nv(const uint16_t *src, int64_t rows, int32_t K, const float *i
  * moe_forward_few -- the whole layer for T <= MOE_FEW_MAX_TOKENS tokens in
  * one kernel launch: router, selection, gate/up + GEGLU, down and the
  * weighted sum, with the dense GEGLU MLP of moe_forward_shared added when
- * I_sh > 0.  Routing (ids, weights) is bit for bit that of moe_route; h is
- * rounded to bf16 as in moe_forward, the experts' outputs are not rounded
- * before they are weighted and summed (fp32), and out is rounded once.
+ * I_sh > 0.  Routing (ids, weights) is bit for bit that of moe_route; h keeps
+ * 16 bits of mantissa (moe_forward rounds it to bf16), the experts' outputs
+ * are not rounded before they are weighted and summed (fp32), and out is
+ * rounded once.
  * Results do not depend on how the work was scheduled: the same call gives
  * the same bits.
  *   weights, scales  as for moe_forward / moe_forward_shared; formats

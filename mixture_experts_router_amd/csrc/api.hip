@@ -172,8 +172,8 @@ FewWorkspace carve_few(const moe_shape *s, void *base, int I_sh) {
     };
     w.counters = reinterpret_cast<uint32_t *>(take(MOE_FEW_ZERO_BYTES));
     w.logits = reinterpret_cast<float *>(take((size_t)s->T * s->E * sizeof(float)));
-    w.h = reinterpret_cast<uint16_t *>(take((size_t)s->T * s->k * s->I * sizeof(uint16_t)));
-    w.h_sh = I_sh > 0 ? reinterpret_cast<uint16_t *>(take((size_t)s->T * I_sh * sizeof(uint16_t))) : nullptr;
+    w.h = reinterpret_cast<uint16_t *>(take((size_t)s->T * s->k * s->I * 2 * sizeof(uint16_t)));
+    w.h_sh = I_sh > 0 ? reinterpret_cast<uint16_t *>(take((size_t)s->T * I_sh * 2 * sizeof(uint16_t))) : nullptr;
     w.y = reinterpret_cast<float *>(take(moe::few_layer_y(weight_view(s, nullptr).fmt, s->T, s->H, s->k, s->I, I_sh)));
     w.bytes = off;
     return w;

@@ -10,7 +10,7 @@
 //            the same bits
 //   gate/up  every workgroup selects the experts itself (top-k of the few
 //            tokens from the logits), then h = gelu_tanh(g) * u for its share
-//            of the (expert, 8 columns) units, rounded to bf16
+//            of the (expert, 8 columns) units
 //   down     y[t, e][16 columns] = W_d h in fp32, the units of all touched
 //            experts shared evenly; with up to 16 assignments instead
 //            out[t][16 columns] = sum over experts of w[t, e] * (W_d h)
@@ -24,8 +24,10 @@
 // have then been taken by workgroups that are running: every wait ends,
 // whatever else runs on the GPU and however few workgroups are resident.
 //
-// h is rounded to bf16, the operand type of the down product's MFMAs; nothing
-// else is rounded below fp32 before out.
+// h goes into the down product's MFMAs as two bf16 values, its rounding to bf16
+// and the rounding of what that left (16 bits of mantissa): one alone would add
+// as much error to out as out's own rounding.  Nothing else is rounded below
+// fp32 before out.
 //
 // Measured at hidden 2816, 128 experts, top-8, expert intermediate 704, one
 // call after another: 1 token 36.7 us in bf16 (95.9 MB of weights) and 28.2
@@ -72,7 +74,7 @@ struct FewArgs {
     float *wts;
     uint32_t *ctr;
     float *logits;
-    uint16_t *h, *h_sh;                         // [T k][I], [T][I_sh]
+    uint16_t *h, *h_sh;                         // [T k][part][I], [T][part][I_sh]
     float *y;                                   // [segment of an expert][T k][H], [segment of the MLP][T][H]
     int T, H, E, k, I, I_sh;
     int n_router, n_gu, n_down, n_combine;      // items of each phase
@@ -312,9 +314,10 @@ struct FewOperand {
 };
 
 // A step out of its slot and (token step xst) the token rows of Src.
-template <int F, class Src>
-__device__ __forceinline__ FewData<F> few_fetch(const Src &src, const uint8_t *q, int st, int xst, const FewOperand<F> &o) {
-    FewData<F> d;
+template <int F, int PARTS, class Src>
+__device__ __forceinline__ FewData<F, PARTS> few_fetch(const Src &src, const uint8_t *q, int st, int xst,
+                                                       const FewOperand<F> &o) {
+    FewData<F, PARTS> d;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         d.c[h] = o.ln.load(q, h);
@@ -322,7 +325,9 @@ __device__ __forceinline__ FewData<F> few_fetch(const Src &src, const uint8_t *q
         if constexpr (FewStep<F>::SOPS > 0) d.sc[h] = o.ln.scale(q, st, h, o.lo);
     }
 #pragma unroll
-    for (int f = 0; f < FewStep<F>::FRAGS; ++f) d.x[f] = src.frag(o.x, xst, f);
+    for (int i = 0; i < PARTS; ++i)
+#pragma unroll
+        for (int f = 0; f < FewStep<F>::FRAGS; ++f) d.x[i][f] = src.frag(o.x, xst, f, i);
     return d;
 }
 
@@ -363,10 +368,10 @@ struct FewGateUp {
         lane(v).issue(m, st, slot, weights(v), weight_bytes(v), scales(v), scale_bytes(v));
     }
     __device__ __forceinline__ FewData<F> fetch(const uint8_t *q, int st, int xst, const FewOperand<F> &o) const {
-        return few_fetch<F>(*this, q, st, xst, o);
+        return few_fetch<F, 1>(*this, q, st, xst, o);
     }
     __device__ __forceinline__ void multiply(const FewData<F> &d, int, const FewOperand<F> &, f32x4 (&acc)[2]) const {
-        few_multiply<F>(d, acc);
+        few_multiply<F, 1>(d, acc);
     }
     __device__ __forceinline__ uint8_t *tokens(int buffer) const {
         return sm.area + kFewWaves * S * SLOT + (size_t)buffer * WINDOW * FewStep<F>::FRAGS * 64 * p.T;
@@ -374,7 +379,7 @@ struct FewGateUp {
     __device__ __forceinline__ FewOperand<F> operand(int, int) const {
         return {tokens(0) + (ln.g * p.T + min((int)ln.r, p.T - 1)) * 16, ln};
     }
-    __device__ __forceinline__ u32x4 frag(const uint8_t *x, int xst, int i) const {
+    __device__ __forceinline__ u32x4 frag(const uint8_t *x, int xst, int i, int) const {
         return *reinterpret_cast<const u32x4 *>(x + 64 * (xst * FewStep<F>::FRAGS + i) * p.T);
     }
     __device__ __forceinline__ void stage(int a, int b, int buffer) const {
@@ -397,9 +402,19 @@ struct FewGateUp {
         if (j) {
             uint16_t *base = shared ? p.h_sh : p.h;
             const size_t row = shared ? (size_t)t : (size_t)t * p.k + j - 1;
-            const uint64_t hv = pack_bf16x2(h[0], h[1]) | (uint64_t)pack_bf16x2(h[2], h[3]) << 32;
-            store_shared(reinterpret_cast<uint64_t *>(MOE_CHECKED(base + row * I + 8 * (u - v * per) + 4 * ln.g, 8, base,
-                                                                  (size_t)p.T * (shared ? 1 : p.k) * I * 2)), hv);
+            uint16_t *to = base + 2 * row * I + 8 * (u - v * per) + 4 * ln.g;
+#pragma unroll
+            for (int part = 0; part < 2; ++part, to += I) {
+                const uint32_t b[2] = {pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3])};
+                store_shared(reinterpret_cast<uint64_t *>(MOE_CHECKED(to, 8, base, (size_t)p.T * (shared ? 1 : p.k) * I * 4)),
+                             b[0] | (uint64_t)b[1] << 32);
+                // what the rounding left (nothing where it left the range)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float r = bf16_to_f32(q & 1 ? b[q >> 1] >> 16 : b[q >> 1] & 0xFFFFu);
+                    h[q] = __builtin_isinf(r) ? 0.f : h[q] - r;
+                }
+            }
         }
     }
 };
@@ -428,9 +443,10 @@ __device__ __forceinline__ void few_gateup(const FewArgs &p, FewSmem &sm, bool s
 // one before h exists.
 //
 // The token rows of gate/up are gone by then, so the rings need not be theirs:
-// 8 tokens in MXFP4 take 61.6 us with six steps, 63.7 with three; in bf16 three
+// 8 tokens in MXFP4 take 61.6 us with six steps, 62.0 with four (which leave 16
+// tokens' rows of intermediate 704 room), 63.7 with three; in bf16 three
 // are enough (117.9 with seven, 118.1), 16 tokens with MLP 186.4 with seven, 183.3.
-constexpr int few_down_ring(int f) { return f == kFewBf16 ? 3 : 6; }
+constexpr int few_down_ring(int f) { return f == kFewBf16 ? 3 : 4; }
 
 template <int F, bool COLUMNS>
 struct FewDown {
@@ -441,7 +457,7 @@ struct FewDown {
     static constexpr int H_BYTES = kFewArea - kFewWaves * S * SLOT;   // LDS for rows of h
     const FewArgs &p;
     FewSmem &sm;
-    const int ne, PW, pitch;      // segments of an expert, steps of a segment, bytes of one's row of h
+    const int ne, PW, pitch;      // segments of an expert, steps of a segment, bytes of one's row of h (two parts)
     const int UE, n, blocks;      // segments of the experts, of all; blocks of columns
     const int r, g;               // this lane's token, its part of a fragment
     uint8_t *hs;
@@ -449,7 +465,7 @@ struct FewDown {
     mutable f32x4 out;            // COLUMNS: sums of this wave's units
 
     __device__ __forceinline__ FewDown(const FewArgs &p, FewSmem &sm)
-        : p(p), sm(sm), ne(p.ne), PW(p.PW), pitch(p.PW * KS * 2 + 16), UE(uniform(sm.n_experts) * p.ne), n(UE + p.ns),
+        : p(p), sm(sm), ne(p.ne), PW(p.PW), pitch(2 * p.PW * KS * 2 + 16), UE(uniform(sm.n_experts) * p.ne), n(UE + p.ns),
           blocks(p.H / 16), r(threadIdx.x & 15), g((threadIdx.x & 63) >> 4), hs(sm.area + kFewWaves * S * FewStep<F>::SLOT) {}
     __device__ __forceinline__ int at(int u, int v) const {
         if constexpr (COLUMNS) return u;
@@ -491,11 +507,11 @@ struct FewDown {
     __device__ __forceinline__ void issue(const FewRows &m, int v, int st, uint8_t *slot) const {
         lane(v).issue(m, st, slot, weights(v), weight_bytes(v), scales(v), scale_bytes(v));
     }
-    __device__ __forceinline__ FewData<F> fetch(const uint8_t *q, int st, int xst, const FewOperand<F> &o) const {
-        return few_fetch<F>(*this, q, st, xst, o);
+    __device__ __forceinline__ FewData<F, 2> fetch(const uint8_t *q, int st, int xst, const FewOperand<F> &o) const {
+        return few_fetch<F, 2>(*this, q, st, xst, o);
     }
-    __device__ __forceinline__ void multiply(const FewData<F> &d, int, const FewOperand<F> &, f32x4 (&acc)[2]) const {
-        few_multiply<F>(d, acc);
+    __device__ __forceinline__ void multiply(const FewData<F, 2> &d, int, const FewOperand<F> &, f32x4 (&acc)[2]) const {
+        few_multiply<F, 2>(d, acc);
     }
     // this lane's row of h: its token's, or, where that is not routed here, the first one (left out by finish)
     __device__ __forceinline__ FewOperand<F> operand(int, int v) const {
@@ -504,8 +520,8 @@ struct FewDown {
         return {hs + (size_t)(rows_before(v) - base + (j ? rank : 0)) * pitch - 2 * KS * PW * piece(v) +
                     2 * few_frag_k<F>(0, g), lane(v)};
     }
-    __device__ __forceinline__ u32x4 frag(const uint8_t *x, int st, int i) const {
-        return *reinterpret_cast<const u32x4 *>(x + 2 * KS * st + 2 * few_frag_k<F>(i, 0));
+    __device__ __forceinline__ u32x4 frag(const uint8_t *x, int st, int i, int part) const {
+        return *reinterpret_cast<const u32x4 *>(x + part * 2 * KS * PW + 2 * KS * st + 2 * few_frag_k<F>(i, 0));
     }
     __device__ __forceinline__ void finish(int u, int v, const f32x4 &acc) const {
         const int t = r, j = routed(v, t);
@@ -533,13 +549,14 @@ struct FewDown {
             const int nr = m ? p.T : uniform(sm.first[e + 1]) - f, I = m ? p.I_sh : p.I;
             const int a = piece(v) * PW, b = min(few_steps(F, I), a + PW);
             const int valid = (min(I, b * KS) - a * KS) / 8, all = (b - a) * (KS / 8);   // 16-byte pieces of a row
-            uint8_t *dst = hs + (size_t)(uniform(rows_before(v)) - base) * pitch;
-            for (int i = 0; i < nr; ++i, dst += pitch) {
+            uint8_t *row = hs + (size_t)(uniform(rows_before(v)) - base) * pitch;
+            for (int i = 0; i < 2 * nr; ++i) {   // both parts of each row
                 const uint16_t *hb = m ? p.h_sh : p.h;
-                const uint16_t *src = hb + (size_t)(m ? i : uniform(sm.sorted[f + i])) * I + a * KS;
+                const uint16_t *src = hb + (size_t)(2 * (m ? i >> 1 : uniform(sm.sorted[f + (i >> 1)])) + (i & 1)) * I + a * KS;
+                uint8_t *dst = row + (i >> 1) * pitch + (i & 1) * 2 * KS * PW;
                 for (int c = 0; c < all; c += 64) {
                     if (c + lane < valid)
-                        dma16<false>(MOE_CHECKED(src + 8 * (c + lane), 16, hb, (size_t)p.T * (m ? 1 : p.k) * I * 2),
+                        dma16<false>(MOE_CHECKED(src + 8 * (c + lane), 16, hb, (size_t)p.T * (m ? 1 : p.k) * I * 4),
                                      dst + 16 * c);
                     else if (c + lane < all)   // past the row: the codes there count nothing
                         *reinterpret_cast<u32x4 *>(dst + 16 * (c + lane)) = u32x4{0u, 0u, 0u, 0u};
@@ -733,7 +750,7 @@ FewPlan few_plan(int f, int T, int H, int k, int I, int I_sh) {
     auto rest = [&](int i) { return kFewArea - kFewWaves * rings[i] * few_slot(f); };
     while (g.ring < kRings && (long long)few_steps(f, H) * step * T > rest(g.ring)) ++g.ring;
     // segments of which T rows of h fit
-    const int most = ((kFewArea - kFewWaves * few_down_ring(f) * few_slot(f)) / T - 16) / step, st = few_steps(f, I), want = (st + most - 1) / most;
+    const int most = ((kFewArea - kFewWaves * few_down_ring(f) * few_slot(f)) / T - 16) / (2 * step), st = few_steps(f, I), want = (st + most - 1) / most;
     g.PW = (st + want - 1) / want;
     g.ne = (st + g.PW - 1) / g.PW;
     g.ns = (few_steps(f, I_sh) + g.PW - 1) / g.PW;
@@ -749,7 +766,7 @@ template <int F, int R = 0>
 void launch_format(const FewArgs &p, int ring, int blocks, hipStream_t st) {
     constexpr int S = kRing[F != kFewBf16][R], W = R == kRings ? kWindow[F != kFewBf16] : 0;
     static_assert(2 * W * FewStep<F>::FRAGS * 64 * kFewTokens <= kFewArea - kFewWaves * S * FewStep<F>::SLOT, "windows");
-    static_assert((kFewArea - kFewWaves * few_down_ring(F) * FewStep<F>::SLOT) / kFewTokens >= 16 + FewStep<F>::K * 2,
+    static_assert((kFewArea - kFewWaves * few_down_ring(F) * FewStep<F>::SLOT) / kFewTokens >= 16 + FewStep<F>::K * 4,
                   "a segment is one step or more");
     if (ring == R) {
         few_layer_kernel<F, S, W><<<blocks, kFewThreads, 0, st>>>(p);

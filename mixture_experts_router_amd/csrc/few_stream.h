@@ -206,24 +206,26 @@ struct FewI4 {
 
 // What a step multiplies, out of its slot and the token rows (bf16, MXFP4,
 // NVFP4).
-template <int F>
+//
+// PARTS: the token values are sums of that many bf16 values.
+template <int F, int PARTS = 1>
 struct FewData {
     u32x4 c[2];
     uint32_t sc[2];
-    u32x4 x[FewStep<F>::FRAGS];
+    u32x4 x[PARTS][FewStep<F>::FRAGS];
 };
 
-template <int F>
-__device__ __forceinline__ void few_multiply(const FewData<F> &d, f32x4 (&acc)[2]) {
+template <int F, int PARTS>
+__device__ __forceinline__ void few_multiply(const FewData<F, PARTS> &d, f32x4 (&acc)[2]) {
+    constexpr int N = FewStep<F>::FRAGS / 2;   // MFMAs of a piece
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        if constexpr (F == kFewBf16) {
-            acc[h] = mfma16x16x32(d.c[h], d.x[h], acc[h]);
-        } else {
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int f = 0; f < 4; ++f) acc[h] = mfma16x16x32(few_operand<F>(d.c[h], d.sc[h], f), d.x[4 * h + f], acc[h]);
+        for (int f = 0; f < N; ++f) {
+            const u32x4 w = few_operand<F>(d.c[h], d.sc[h], f);
+#pragma unroll
+            for (int i = 0; i < PARTS; ++i) acc[h] = mfma16x16x32(w, d.x[i][N * h + f], acc[h]);
         }
-    }
 }
 
 // A workgroup's run of units, each an MFMA tile of sixteen weight rows summed

@@ -161,7 +161,7 @@ struct GemvUnits {
         FewI4 codes;
     };
     struct I4Data {
-        u32x4 c[2], x[FRAGS], scale[NG];
+        u32x4 c[2], x[1][FRAGS], scale[NG];
         uint32_t own[NS + 1], zero[NS + 1];   // the words this lane loaded: of row lane % 16, group lane / 16 + 4 i
     };
     using Data = std::conditional_t<I4, I4Data, FewData<F>>;
@@ -238,12 +238,12 @@ struct GemvUnits {
         }
         const uint8_t *x = o.x + (size_t)(WINDOW ? xst : st - c0) * FRAGS * 64 * p.T;
 #pragma unroll
-        for (int f = 0; f < FRAGS; ++f) d.x[f] = *reinterpret_cast<const u32x4 *>(x + f * 64 * p.T);
+        for (int f = 0; f < FRAGS; ++f) d.x[0][f] = *reinterpret_cast<const u32x4 *>(x + f * 64 * p.T);
         return d;
     }
     __device__ __forceinline__ void multiply(const Data &d, int st, const Operand &o, f32x4 (&acc)[2]) const {
         if constexpr (!I4) {
-            few_multiply<F>(d, acc);
+            few_multiply<F, 1>(d, acc);
         } else {
             // group by group: the sums of (16 + code) x, and of x (the ones' rows are alike)
             f32x4 part[NG], tokens[NG];
@@ -255,8 +255,8 @@ struct GemvUnits {
                 for (int i = 0; i < 4; ++i) {
                     const int f = 4 * h + i, j = f * 32 / GROUP;
                     if (f * 32 % GROUP == 0) part[j] = tokens[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-                    part[j] = mfma16x16x32(o.codes.operand(c[i]), d.x[f], part[j]);
-                    tokens[j] = mfma16x16x32(u32x4{kOnes, kOnes, kOnes, kOnes}, d.x[f], tokens[j]);
+                    part[j] = mfma16x16x32(o.codes.operand(c[i]), d.x[0][f], part[j]);
+                    tokens[j] = mfma16x16x32(u32x4{kOnes, kOnes, kOnes, kOnes}, d.x[0][f], tokens[j]);
                 }
             }
             // the groups' offsets, - scale (16 + zero) times the token sums, are an fp32 product over the groups: lane

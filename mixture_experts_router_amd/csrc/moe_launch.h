@@ -121,7 +121,7 @@ struct FewLayer {
     float *w;                // or nullptr
     uint32_t *counters;      // kFewCounterBytes, zero before the launch and after it
     float *logits;           // [T][E]
-    uint16_t *h, *h_sh;      // [T*k][I], [T][I_sh]
+    uint16_t *h, *h_sh;      // [T*k][2][I], [T][2][I_sh]
     float *y;                // few_layer_y bytes: the down products before they are added
     int T, H, E, k, I, I_sh;
 };
