@@ -26,14 +26,15 @@
 //
 // h goes into the down product's MFMAs as two bf16 values, its rounding to bf16
 // and the rounding of what that left (16 bits of mantissa): one alone would add
-// as much error to out as out's own rounding.  Nothing else is rounded below
-// fp32 before out.
+// as much error to out as out's own rounding (2.4e-3 of out's norm against
+// 1.65e-3).  It costs 16 tokens with the MLP 4% (189 us against 181), fewer
+// tokens nothing.  Nothing else is rounded below fp32 before out.
 //
 // Measured at hidden 2816, 128 experts, top-8, expert intermediate 704, one
-// call after another: 1 token 36.7 us in bf16 (95.9 MB of weights) and 28.2
-// in MXFP4 (26.0 MB), 8 tokens 118 (615 MB: 5.2 TB/s) and 62 (164 MB), 5
-// tokens in NVFP4 55 (119 MB), 16 tokens with the dense MLP in bf16 183
-// (1.02 GB: 5.6 TB/s).  Of the 8 bf16 tokens' time 13 us pass before the first
+// call after another: 1 token 37 us in bf16 (95.9 MB of weights) and 28 in
+// MXFP4 (26.0 MB), 8 tokens 116 (615 MB: 5.3 TB/s) and 62 (164 MB), 5 tokens
+// in NVFP4 56 (119 MB), 16 tokens with the dense MLP in bf16 189 (1.02 GB: 5.4
+// TB/s).  Of the 8 bf16 tokens' time 13 us pass before the first
 // expert weight is requested (start 2, ticket and router 5, top-k 6), 58 in
 // gate/up (7.0 TB/s), 9 until h has arrived everywhere, 28 in down (7.3 TB/s,
 // first weights requested before h is there), 6 in combine.  What bounds it:
@@ -442,10 +443,10 @@ __device__ __forceinline__ void few_gateup(const FewArgs &p, FewSmem &sm, bool s
 // weights of a pass are requested before its h is staged, those of the first
 // one before h exists.
 //
-// The token rows of gate/up are gone by then, so the rings need not be theirs:
-// 8 tokens in MXFP4 take 61.6 us with six steps, 62.0 with four (which leave 16
-// tokens' rows of intermediate 704 room), 63.7 with three; in bf16 three
-// are enough (117.9 with seven, 118.1), 16 tokens with MLP 186.4 with seven, 183.3.
+// The token rows of gate/up are gone by then, so the rings need not be theirs.
+// 16 tokens with MLP in bf16 take 189.0 us with three steps, 190.1 with five; 8
+// tokens in MXFP4 62.6 with four, 63.1 with five (which leave 16 tokens' rows
+// of intermediate 704 no room in one piece).
 constexpr int few_down_ring(int f) { return f == kFewBf16 ? 3 : 4; }
 
 template <int F, bool COLUMNS>
@@ -729,7 +730,7 @@ __global__ __launch_bounds__(kFewThreads) void few_layer_kernel(FewArgs p) {
 // by slot size), else the one that leaves room for windows of them.  A short
 // ring next to whole rows is better than a deep one next to windows, which cost
 // a barrier each and leave the last units unsplit: 16 tokens, hidden 2816, bf16
-// with MLP 183 us (3 steps) against 190 (6 steps); 12 tokens, hidden 4096,
+// with MLP 183 us (3 steps) against 190 (6 steps; h in one part); 12 tokens, hidden 4096,
 // NVFP4 74 (2) against 83 (4).  Windows against rows read from global memory, 16
 // tokens, hidden 5120: bf16 178 us against 230, MXFP4 95 against 153.
 constexpr int kRings = 3, kRing[2][kRings + 1] = {{7, 5, 3, 6}, {6, 4, 2, 4}}, kWindow[2] = {8, 4};
